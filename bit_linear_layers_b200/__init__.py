@@ -14,6 +14,12 @@ if the library is missing, importing the binding raises.
     bin_xnor_gemm(a, b, K)                 -> dot (int32), W1A1
     bin_linear_w1a16_backward(x, packed, alpha, dy) -> dx, dW, dalpha (straight-through)
     W1A16Stack(levels).run()               decode through a stack of layers in one launch
+    layer_norm(x, weight, bias)            -> y (and the rows' statistics)
+    layer_norm_backward(x, weight, mean, rstd, dy) -> dx, dweight, dbias
+    embedding(ids, table, scale=s)         -> y = s * table[ids]
+    embedding_backward(ids, dy, V)         -> dtable, the gradient of the whole table
+    grad_clip(tensors, max_norm)           -> norm, coef; the tensors scaled down to max_norm
+    grad_norm(tensors)                     -> norm
 """
 from __future__ import annotations
 
@@ -49,10 +55,19 @@ BL_OP_W158A8 = 5
 BL_OP_W1A8_EX = 6
 BL_OP_W1A16_STACK = 7
 BL_OP_W1A16_BACKWARD = 8
+BL_OP_LAYER_NORM_BACKWARD = 9
+BL_OP_EMBEDDING_BACKWARD = 10
+BL_OP_GRAD_CLIP = 11
 
 BL_W1A8_TERNARY = 1
 BL_W1A8_PER_TENSOR = 2
 BL_W1A8_NONNEG = 4
+
+BL_TYPE_BF16 = 0
+BL_TYPE_F32 = 1
+BL_IDS_I32 = 0
+BL_IDS_I64 = 1
+BL_EMBED_ACCUMULATE = 1
 
 
 class StackJob(ctypes.Structure):
@@ -65,6 +80,11 @@ class StackLevel(ctypes.Structure):
     """bl_stack_level: one input vector and the linears that read it."""
     _fields_ = [("x", ctypes.c_void_p), ("K", ctypes.c_int64), ("first_job", ctypes.c_int32),
                 ("num_jobs", ctypes.c_int32)]
+
+
+class GradTensor(ctypes.Structure):
+    """bl_grad_tensor: one gradient tensor and where its scaled copy goes."""
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
 # every symbol include/bitlinear.h declares, with its ctypes signature
@@ -89,6 +109,13 @@ SIGNATURES = {
     "bin_linear_w1a16_backward": ([_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _sz, _p], _int),
     "bitlinear_w1a8_ex": ([_p, _p, _p, _p, _i64, _i64, _i64, ctypes.c_uint, _p, _sz, _p, _p, _p, _p], _int),
     "bitlinear_w158a8": ([_p, _p, _p, _p, _i64, _i64, _i64, _p, _sz, _p], _int),
+    "bl_layer_norm": ([_p, _int, _i64, _p, _p, _p, _int, _i64, _p, _p, _i64, _i64, ctypes.c_float, _p], _int),
+    "bl_layer_norm_backward": ([_p, _int, _i64, _p, _p, _p, _p, _int, _i64, _p, _i64, _p, _p, _i64, _i64, _p, _sz, _p],
+                               _int),
+    "bl_embedding": ([_p, _int, _p, _int, _p, _int, _i64, _i64, _i64, ctypes.c_float, _p], _int),
+    "bl_embedding_backward": ([_p, _int, _p, _int, _p, _int, _i64, _i64, _i64, ctypes.c_float, _i64, ctypes.c_uint, _p,
+                               _sz, _p], _int),
+    "bl_grad_clip": ([_p, _int, ctypes.c_float, _p, _p, _sz, _p], _int),
     "bitlinear_w158a8_debug": ([_p, _p, _p, _p, _i64, _i64, _i64, _p, _sz, _p, _p, _p, _p, _p, _p], _int),
 }
 
@@ -406,6 +433,227 @@ def bin_xnor_gemm(a: torch.Tensor, b: torch.Tensor, K: int, *, out=None):
                            _dev_ptr(out, torch.int32, "out"), M, N, K, _stream(a.device))
     _check("bin_xnor_gemm", rc)
     return out
+
+
+# ---- full-precision operators of a training step
+
+_TYPE = {torch.bfloat16: BL_TYPE_BF16, torch.float32: BL_TYPE_F32}
+_ID_TYPE = {torch.int32: BL_IDS_I32, torch.int64: BL_IDS_I64}
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """Call an entry point on the current stream of `device`, with `device` current."""
+    if device.index == torch.cuda.current_device():
+        rc = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != BL_OK:
+        raise BitLinearError(name, rc)
+
+
+def _typed(t: torch.Tensor, types: dict, name: str, device: torch.device) -> int:
+    """The BL_* code of t's element type; t has to be on `device`."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}" if device.type == "cuda"
+                         else f"{name} must be a CUDA tensor")
+    code = types.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in types)}, got {t.dtype}")
+    return code
+
+
+def _rows(t: torch.Tensor, M: int, K: int, name: str) -> int:
+    """Row pitch of an [M, K] tensor whose rows are dense."""
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != K:
+        raise ValueError(f"{name} must be [{M}, {K}], got {list(t.shape)}")
+    ld, s = t.stride()
+    if (s != 1 and K > 1) or (ld < K and M > 1):
+        raise ValueError(f"{name} must have dense rows that do not overlap")
+    return max(ld, K)
+
+
+def _dense(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, name: str, device: torch.device):
+    """Pointer of a dense tensor of that shape and type (None: none)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _ws(op: int, M: int, N: int, K: int, device: torch.device, ws):
+    need = lib.bl_workspace_bytes(op, M, N, K)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
+               eps: float = 1e-5, out=None, out_dtype=None, stats: bool = False, mean=None, rstd=None):
+    """Layer norm of the rows of x [M, K] (bf16 or fp32; rows may have a
+    pitch): y = (x - mu) / sqrt(var + eps) * weight + bias, with weight and
+    bias fp32 [K] or None. y has out_dtype (default: x's) or is written to
+    `out`, which may be x. With stats=True returns (y, mean, rstd), the fp32
+    [M] statistics that layer_norm_backward takes."""
+    dev = x.device
+    xt = _typed(x, _TYPE, "x", dev)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {list(x.shape)}")
+    M, K = x.shape
+    ldx = _rows(x, M, K, "x")
+    if out is None:
+        out = torch.empty((M, K), dtype=out_dtype or x.dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+    yt, ldy = _typed(out, _TYPE, "out", dev), _rows(out, M, K, "out")
+    if stats:
+        mean = torch.empty(M, dtype=torch.float32, device=dev) if mean is None else mean
+        rstd = torch.empty(M, dtype=torch.float32, device=dev) if rstd is None else rstd
+    f32 = torch.float32
+    _call("bl_layer_norm", dev, x.data_ptr(), xt, ldx, _dense(weight, (K,), f32, "weight", dev),
+          _dense(bias, (K,), f32, "bias", dev), out.data_ptr(), yt, ldy, _dense(mean, (M,), f32, "mean", dev),
+          _dense(rstd, (M,), f32, "rstd", dev), M, K, eps)
+    return (out, mean, rstd) if stats else out
+
+
+def layer_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor, rstd: torch.Tensor,
+                        dy: torch.Tensor, *, want_dx: bool = True, want_dw: bool = True, dx=None, dweight=None,
+                        dbias=None, ws=None):
+    """Gradients of layer_norm: returns (dx [M, K] of x's type or None,
+    dweight [K] fp32 or None, dbias [K] fp32 or None). mean and rstd are the
+    statistics the forward pass returned."""
+    dev = x.device
+    xt, gt = _typed(x, _TYPE, "x", dev), _typed(dy, _TYPE, "dy", dev)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {list(x.shape)}")
+    M, K = x.shape
+    ldx, lddy = _rows(x, M, K, "x"), _rows(dy, M, K, "dy")
+    f32 = torch.float32
+    lddx = K
+    if not want_dx:
+        dx = None
+    elif dx is None:
+        dx = torch.empty((M, K), dtype=x.dtype, device=dev)
+    else:
+        if _typed(dx, _TYPE, "dx", dev) != xt:
+            raise ValueError(f"dx must be {x.dtype}, got {dx.dtype}")
+        lddx = _rows(dx, M, K, "dx")
+    if want_dw:
+        dweight = torch.empty(K, dtype=f32, device=dev) if dweight is None else dweight
+        dbias = torch.empty(K, dtype=f32, device=dev) if dbias is None else dbias
+        ws = _ws(BL_OP_LAYER_NORM_BACKWARD, M, 0, K, dev, ws)
+    else:
+        dweight = dbias = ws = None
+    _call("bl_layer_norm_backward", dev, x.data_ptr(), xt, ldx, _dense(weight, (K,), f32, "weight", dev),
+          _dense(mean, (M,), f32, "mean", dev), _dense(rstd, (M,), f32, "rstd", dev), dy.data_ptr(), gt, lddy,
+          None if dx is None else dx.data_ptr(), lddx, _dense(dweight, (K,), f32, "dweight", dev),
+          _dense(dbias, (K,), f32, "dbias", dev), M, K, None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
+    return dx, dweight, dbias
+
+
+def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, out=None, out_dtype=None):
+    """y = scale * table[ids]: ids int32 or int64 of any shape, table [V, D]
+    bf16 or fp32; y [*ids.shape, D] of out_dtype (default: the table's). Ids
+    outside [0, V) give rows of zeros and are recorded in device_error()."""
+    dev = table.device
+    it, tt = _typed(ids, _ID_TYPE, "ids", dev), _typed(table, _TYPE, "table", dev)
+    if table.dim() != 2 or not table.is_contiguous() or not ids.is_contiguous():
+        raise ValueError("table must be a contiguous [V, D] tensor and ids contiguous")
+    V, D = table.shape
+    shape = (*ids.shape, D)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or table.dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+    yt = _typed(out, _TYPE, "out", dev)
+    _call("bl_embedding", dev, ids.data_ptr(), it, table.data_ptr(), tt, _dense(out, shape, out.dtype, "out", dev), yt,
+          ids.numel(), V, D, scale)
+    return out
+
+
+def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, V: int, *, scale: float = 1.0,
+                       padding_id: int | None = None, out=None, out_dtype=None, accumulate: bool = False, ws=None):
+    """Gradient of embedding with respect to the whole table: [V, D] of
+    out_dtype (default: fp32), row v = scale * the sum of dy over the tokens
+    that equal v, zeros elsewhere. With accumulate=True the sums are added to
+    `out`. Tokens equal to padding_id give nothing."""
+    dev = dy.device
+    it, gt = _typed(ids, _ID_TYPE, "ids", dev), _typed(dy, _TYPE, "dy", dev)
+    D = dy.shape[-1] if dy.dim() else 0
+    if tuple(dy.shape) != (*ids.shape, D) or not dy.is_contiguous() or not ids.is_contiguous():
+        raise ValueError(f"dy must be a contiguous [*ids.shape, D] tensor and ids contiguous, got {list(dy.shape)} for "
+                         f"ids {list(ids.shape)}")
+    if padding_id is not None and not 0 <= padding_id < V:
+        raise ValueError(f"padding_id must be in [0, {V}), got {padding_id}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate=True adds to `out`: give it")
+        out = torch.empty((V, D), dtype=out_dtype or torch.float32, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+    tt = _typed(out, _TYPE, "out", dev)
+    T = ids.numel()
+    ws = _ws(BL_OP_EMBEDDING_BACKWARD, T, V, D, dev, ws)
+    _call("bl_embedding_backward", dev, ids.data_ptr(), it, dy.data_ptr(), gt,
+          _dense(out, (V, D), out.dtype, "out", dev), tt, T, V, D, scale, -1 if padding_id is None else padding_id,
+          BL_EMBED_ACCUMULATE if accumulate else 0, ws.data_ptr(), ws.numel())
+    return out
+
+
+def _grad_clip(tensors, outs, max_norm, stats, ws):
+    n = len(tensors)
+    if n == 0:
+        raise ValueError("no tensors")
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    rows = []
+    for t, o in zip(tensors, outs):
+        code = _TYPE.get(t.dtype)
+        if code is None or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"tensors must be contiguous bf16 or fp32 tensors on {dev}, got {t.dtype} {list(t.shape)} "
+                             f"on {t.device}")
+        numel = t.numel()
+        if o is t:
+            rows.append((t.data_ptr(), t.data_ptr(), numel, code))
+        elif o is None:
+            rows.append((t.data_ptr(), 0, numel, code))
+        else:
+            if o.dtype != t.dtype or o.device != dev or o.numel() != numel or not o.is_contiguous():
+                raise ValueError("an output must be a contiguous tensor of its gradient's type, size and device")
+            rows.append((t.data_ptr(), o.data_ptr(), numel, code))
+    table = (GradTensor * n)(*rows)
+    if stats is None:
+        stats = torch.empty(2, dtype=torch.float32, device=dev)
+    ws = _ws(BL_OP_GRAD_CLIP, n, 0, 0, dev, ws)
+    _call("bl_grad_clip", dev, ctypes.byref(table), n, max_norm, _dense(stats, (2,), torch.float32, "stats", dev),
+          ws.data_ptr(), ws.numel())
+    return stats[0], stats[1]
+
+
+def grad_clip(tensors, max_norm: float, *, out=None, stats=None, ws=None):
+    """Scale the tensors (bf16 or fp32, one device) by coef = min(1, max_norm /
+    (norm + 1e-6)), norm the 2-norm over all of them: in place, or into the
+    tensors of `out` (one for each; None: not written). Returns (norm, coef)
+    as fp32 device scalars (the two elements of `stats`); nothing waits for
+    the GPU. A NaN among the gradients makes everything NaN."""
+    tensors = list(tensors)
+    outs = tensors if out is None else list(out)
+    if len(outs) != len(tensors):
+        raise ValueError(f"{len(outs)} outputs for {len(tensors)} tensors")
+    return _grad_clip(tensors, outs, max_norm, stats, ws)
+
+
+def grad_norm(tensors, *, stats=None, ws=None):
+    """The 2-norm over all elements of the tensors, as an fp32 device scalar."""
+    tensors = list(tensors)
+    return _grad_clip(tensors, [None] * len(tensors), float("inf"), stats, ws)[0]
 
 
 def device_error(clear: bool = True, device=None) -> tuple[int, int]:

@@ -8,14 +8,17 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
 #include "bitlinear.h"
 #include "bl_backward.cuh"
 #include "bl_common.cuh"
+#include "bl_embedding.cuh"
 #include "bl_gemm_ts.cuh"
 #include "bl_gemv.cuh"
 #include "bl_gemv_lut.cuh"
@@ -23,6 +26,8 @@
 #include "bl_gemv_stream.cuh"
 #include "bl_gemv_stream_mma.cuh"
 #include "bl_gemv_w1a8_mma.cuh"
+#include "bl_gradclip.cuh"
+#include "bl_layernorm.cuh"
 #include "bl_lnquant.cuh"
 #include "bl_pack.cuh"
 #include "bl_xnor.cuh"
@@ -527,6 +532,73 @@ int w1a8_impl(const uint16_t* x, const uint32_t* packed, const float* beta, floa
                  : launch_ts<1>(codes, packed, M, N, K, nullptr, gam, beta, y, acc_out, sms, s);
 }
 
+// ---- full-precision operators of a training step --------------------------------
+constexpr int64_t kMaxIds = (int64_t(1) << 31) - 1;
+
+inline bool type_ok(int type) { return type == BL_TYPE_BF16 || type == BL_TYPE_F32; }
+inline int type_bytes(int type) { return type == BL_TYPE_F32 ? 4 : 2; }
+inline bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes) == 0; }
+
+// rows of K elements with a pitch of ld elements, all below 2^40 elements
+int check_rows(int64_t M, int64_t K, int64_t ld) {
+  if (ld < K) return BL_ERR_INVALID_ARG;
+  if (ld > kMaxProduct || (M > 0 && ld >= kMaxProduct / M)) return BL_ERR_UNSUPPORTED;
+  return BL_OK;
+}
+int check_norm_shape(int64_t M, int64_t K) {
+  if (M < 0 || K < 1) return BL_ERR_INVALID_ARG;
+  return M > kMaxDim || K > kMaxDim ? BL_ERR_UNSUPPORTED : BL_OK;
+}
+
+struct NormWs {
+  int64_t parts;  // partial rows of dweight and dbias
+  size_t shift, part, bytes;
+};
+NormWs norm_ws(int64_t M, int64_t K) {
+  NormWs w{};
+  if (M < 1 || K < 1 || M > kMaxDim || K > kMaxDim || M >= kMaxProduct / K) return w;
+  w.parts = std::min<int64_t>(cdiv(M, 64), 128);
+  w.shift = 0;
+  w.part = align256(size_t(M) * 4);
+  w.bytes = w.part + align256(size_t(2 * w.parts) * size_t(K) * 4);
+  return w;
+}
+
+struct EmbedWs {
+  int64_t chunks;
+  size_t key[2], val[2], touched, num_heavy, heavy, part, bytes;
+};
+EmbedWs embed_ws(int64_t T, int64_t V, int64_t D) {
+  EmbedWs w{};
+  if (T < 1 || V < 1 || D < 1 || T > kMaxIds || V > kMaxIds || D > kMaxDim || T >= kMaxProduct / D) return w;
+  w.chunks = cdiv(T, kEgChunk);
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t a = at;
+    at += align256(bytes);
+    return a;
+  };
+  for (int i = 0; i < 2; ++i) {
+    w.key[i] = take(size_t(T) * 4);
+    w.val[i] = take(size_t(T) * 4);
+  }
+  w.touched = take(size_t(cdiv(V, 32)) * 4);
+  w.num_heavy = take(4);
+  w.heavy = take(size_t(w.chunks) * sizeof(EmbedHeavy));
+  w.part = take(size_t(2 * w.chunks) * size_t(D) * 4);
+  w.bytes = at;
+  return w;
+}
+
+inline int64_t gc_launches(int64_t n) { return n < 1 ? 1 : cdiv(n, kGcMaxTensors); }
+
+// f(uint16_t or float of `a`, of `b`)
+template <typename F>
+int with_types(int a, int b, F&& f) {
+  if (a == BL_TYPE_F32) return b == BL_TYPE_F32 ? f(float{}, float{}) : f(float{}, uint16_t{});
+  return b == BL_TYPE_F32 ? f(uint16_t{}, float{}) : f(uint16_t{}, uint16_t{});
+}
+
 }  // namespace
 }  // namespace bl
 
@@ -568,6 +640,9 @@ size_t bl_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
              align256(size_t(K) * 4) + align256(size_t(K) * Mp * 2) + align256(size_t(N) * Mp * 2) +
              align256(size_t(K / kSsRowsA) * size_t(N) * 4);
     }
+    case BL_OP_LAYER_NORM_BACKWARD: return norm_ws(M, K).bytes;
+    case BL_OP_EMBEDDING_BACKWARD: return embed_ws(M, N, K).bytes;
+    case BL_OP_GRAD_CLIP: return size_t(gc_launches(M)) * kGcMaxCtas * sizeof(double);
     default: return 0;
   }
 }
@@ -947,6 +1022,265 @@ int bin_xnor_gemm(const uint32_t* a, const uint32_t* b, int32_t* dot, int64_t M,
   const dim3 grid(static_cast<unsigned>(cdiv(N, kXnorTile)), static_cast<unsigned>(cdiv(M, kXnorTile)), 1);
   xnor_gemm_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a, b, dot, M, N, K);
   return launch_status();
+}
+
+int bl_layer_norm(const void* x, int x_type, int64_t ldx, const float* weight, const float* bias, void* y, int y_type,
+                  int64_t ldy, float* mean, float* rstd, int64_t M, int64_t K, float eps, void* stream) {
+  int rc = check_norm_shape(M, K);
+  if (rc != BL_OK) return rc;
+  if (!type_ok(x_type) || !type_ok(y_type) || !(eps > 0.f) || !(eps < INFINITY)) return BL_ERR_INVALID_ARG;
+  if ((rc = check_rows(M, K, ldx)) != BL_OK || (rc = check_rows(M, K, ldy)) != BL_OK) return rc;
+  if (M == 0) return BL_OK;
+  if (!x || !y || !aligned_to(x, type_bytes(x_type)) || !aligned_to(y, type_bytes(y_type)) || !aligned_to(weight, 4) ||
+      !aligned_to(bias, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return BL_ERR_INVALID_ARG;
+  if (x == y && (x_type != y_type || ldx != ldy)) return BL_ERR_INVALID_ARG;
+  rc = device_setup(nullptr);
+  if (rc != BL_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_types(x_type, y_type, [&](auto tx, auto ty) {
+    using TX = decltype(tx);
+    using TY = decltype(ty);
+    layer_norm_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
+        static_cast<const TX*>(x), ldx, weight, bias, static_cast<TY*>(y), ldy, mean, rstd, K, eps);
+    return launch_status();
+  });
+}
+
+int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* weight, const float* mean,
+                           const float* rstd, const void* dy, int dy_type, int64_t lddy, void* dx, int64_t lddx,
+                           float* dweight, float* dbias, int64_t M, int64_t K, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_norm_shape(M, K);
+  if (rc != BL_OK) return rc;
+  if (!type_ok(x_type) || !type_ok(dy_type)) return BL_ERR_INVALID_ARG;
+  if ((rc = check_rows(M, K, ldx)) != BL_OK || (rc = check_rows(M, K, lddy)) != BL_OK ||
+      (dx && (rc = check_rows(M, K, lddx)) != BL_OK))
+    return rc;
+  if (!aligned_to(weight, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4)) return BL_ERR_INVALID_ARG;
+  if (dweight && dweight == dbias) return BL_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {  // an empty batch: zero gradients of the weight and the bias
+    for (float* g : {dweight, dbias})
+      if (g && cudaMemsetAsync(g, 0, size_t(K) * 4, s) != cudaSuccess) {
+        cudaGetLastError();
+        return BL_ERR_CUDA;
+      }
+    return BL_OK;
+  }
+  if (!x || !mean || !rstd || !dy || !aligned_to(x, type_bytes(x_type)) || !aligned_to(dy, type_bytes(dy_type)) ||
+      !aligned_to(dx, type_bytes(x_type)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || dx == x ||
+      (dx && dx == dy))
+    return BL_ERR_INVALID_ARG;
+  const bool want_dw = dweight || dbias;
+  if (!dx && !want_dw) return BL_OK;
+  const NormWs w = norm_ws(M, K);
+  if (w.bytes == 0) return BL_ERR_UNSUPPORTED;
+  if (want_dw && (!ws || !aligned16(ws) || ws_bytes < w.bytes)) return BL_ERR_INVALID_ARG;
+  rc = device_setup(nullptr);
+  if (rc != BL_OK) return rc;
+  float* shift = want_dw ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.shift) : nullptr;
+  float* part = want_dw ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part) : nullptr;
+  return with_types(x_type, dy_type, [&](auto tx, auto ty) {
+    using TX = decltype(tx);
+    using TY = decltype(ty);
+    layer_norm_dx_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
+        static_cast<const TX*>(x), ldx, weight, mean, rstd, static_cast<const TY*>(dy), lddy, static_cast<TX*>(dx),
+        lddx, shift, K);
+    int st = launch_status();
+    if (st != BL_OK || !want_dw) return st;
+    layer_norm_dw_kernel<TX, TY><<<dim3(unsigned(cdiv(K, 32)), unsigned(w.parts)), kNormThreads, 0, s>>>(
+        static_cast<const TX*>(x), ldx, mean, rstd, shift, static_cast<const TY*>(dy), lddy, part, M, K);
+    if ((st = launch_status()) != BL_OK) return st;
+    layer_norm_dw_sum_kernel<<<dim3(unsigned(cdiv(K, 32)), 2), kNormThreads, 0, s>>>(part, w.parts, K, dweight, dbias);
+    return launch_status();
+  });
+}
+
+int bl_embedding(const void* ids, int id_type, const void* table, int table_type, void* y, int y_type, int64_t T,
+                 int64_t V, int64_t D, float scale, void* stream) {
+  if (T < 0 || V < 1 || D < 1) return BL_ERR_INVALID_ARG;
+  if (T > kMaxIds || V > kMaxIds || D > kMaxDim || V >= kMaxProduct / D || (T > 0 && T >= kMaxProduct / D))
+    return BL_ERR_UNSUPPORTED;
+  if ((id_type != BL_IDS_I32 && id_type != BL_IDS_I64) || !type_ok(table_type) || !type_ok(y_type))
+    return BL_ERR_INVALID_ARG;
+  if (T == 0) return BL_OK;
+  if (!ids || !table || !y || !aligned_to(ids, id_type == BL_IDS_I64 ? 8 : 4) ||
+      !aligned_to(table, type_bytes(table_type)) || !aligned_to(y, type_bytes(y_type)))
+    return BL_ERR_INVALID_ARG;
+  int rc = device_setup(nullptr);
+  if (rc != BL_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool vec = D % 8 == 0 && aligned16(table) && aligned16(y);
+  return with_types(table_type, y_type, [&](auto tt, auto ty) {
+    using TT = decltype(tt);
+    using TY = decltype(ty);
+    auto run = [&](auto ti, auto e) {
+      using TI = decltype(ti);
+      embedding_kernel<TI, TT, TY, decltype(e)::value><<<static_cast<unsigned>(T), kEmbThreads, 0, s>>>(
+          static_cast<const TI*>(ids), static_cast<const TT*>(table), static_cast<TY*>(y), T, V, D, scale);
+      return launch_status();
+    };
+    using E1 = std::integral_constant<int, 1>;
+    using E8 = std::integral_constant<int, 8>;
+    if (id_type == BL_IDS_I64) return vec ? run(int64_t{}, E8{}) : run(int64_t{}, E1{});
+    return vec ? run(int32_t{}, E8{}) : run(int32_t{}, E1{});
+  });
+}
+
+int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_type, void* dtable, int table_type,
+                          int64_t T, int64_t V, int64_t D, float scale, int64_t padding_id, unsigned flags, void* ws,
+                          size_t ws_bytes, void* stream) {
+  if (T < 0 || V < 1 || D < 1 || padding_id >= V || (flags & ~BL_EMBED_ACCUMULATE)) return BL_ERR_INVALID_ARG;
+  if (T > kMaxIds || V > kMaxIds || D > kMaxDim || V >= kMaxProduct / D || (T > 0 && T >= kMaxProduct / D))
+    return BL_ERR_UNSUPPORTED;
+  if ((id_type != BL_IDS_I32 && id_type != BL_IDS_I64) || !type_ok(dy_type) || !type_ok(table_type) || !dtable ||
+      !aligned_to(dtable, type_bytes(table_type)))
+    return BL_ERR_INVALID_ARG;
+  const bool acc = (flags & BL_EMBED_ACCUMULATE) != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (!acc && cudaMemsetAsync(dtable, 0, size_t(V) * size_t(D) * size_t(type_bytes(table_type)), s) != cudaSuccess) {
+      cudaGetLastError();
+      return BL_ERR_CUDA;
+    }
+    return BL_OK;
+  }
+  const EmbedWs w = embed_ws(T, V, D);
+  if (!ids || !dy || !aligned_to(ids, id_type == BL_IDS_I64 ? 8 : 4) || !aligned_to(dy, type_bytes(dy_type)) || !ws ||
+      !aligned16(ws) || ws_bytes < w.bytes)
+    return BL_ERR_INVALID_ARG;
+  int sms = 0;
+  int rc = device_setup(&sms);
+  if (rc != BL_OK) return rc;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  EmbedSort p;
+  for (int i = 0; i < 2; ++i) {
+    p.key[i] = reinterpret_cast<uint32_t*>(base + w.key[i]);
+    p.val[i] = reinterpret_cast<uint32_t*>(base + w.val[i]);
+  }
+  p.touched = reinterpret_cast<uint32_t*>(base + w.touched);
+  p.num_heavy = reinterpret_cast<uint32_t*>(base + w.num_heavy);
+  p.heavy = reinterpret_cast<EmbedHeavy*>(base + w.heavy);
+  float* part = reinterpret_cast<float*>(base + w.part);
+  // keys are 0 .. V: equal digits of at most 8 bits
+  int bits = 1;
+  while ((V >> bits) != 0) ++bits;
+  const int passes = (bits + 7) / 8, digit_bits = (bits + passes - 1) / passes;
+  const uint32_t t32 = static_cast<uint32_t>(T), v32 = static_cast<uint32_t>(V);
+  if (id_type == BL_IDS_I64)
+    embed_sort_kernel<int64_t><<<kEsCluster, kEsThreads, 0, s>>>(static_cast<const int64_t*>(ids), t32, v32, padding_id,
+                                                                 passes, digit_bits, p);
+  else
+    embed_sort_kernel<int32_t><<<kEsCluster, kEsThreads, 0, s>>>(static_cast<const int32_t*>(ids), t32, v32, padding_id,
+                                                                 passes, digit_bits, p);
+  if ((rc = launch_status()) != BL_OK) return rc;
+  const uint32_t* key = p.key[(passes + 1) & 1];
+  const uint32_t* val = p.val[(passes + 1) & 1];
+  const int64_t sum_blocks = cdiv(w.chunks * cdiv(D, kEgCols), kEgWarps);
+  const int64_t zero_blocks = acc ? 0 : std::min<int64_t>(cdiv(V, kEgWarps), int64_t(sms) * 8);
+  const bool vec = D % 8 == 0 && aligned16(dy) && aligned16(dtable);
+  return with_types(dy_type, table_type, [&](auto tg, auto tt) {
+    using TG = decltype(tg);
+    using TT = decltype(tt);
+    auto run = [&](auto e, auto a) {
+      constexpr int E = decltype(e)::value;
+      constexpr bool ACC = decltype(a)::value;
+      embed_grad_kernel<TG, TT, E, ACC><<<static_cast<unsigned>(sum_blocks + zero_blocks), kEgWarps * 32, 0, s>>>(
+          key, val, p.touched, static_cast<const TG*>(dy), static_cast<TT*>(dtable), part, t32, v32, D, scale,
+          static_cast<uint32_t>(sum_blocks));
+      int st = launch_status();
+      if (st != BL_OK || w.chunks < 3) return st;  // a long segment spans three chunks
+      const int64_t most = (w.chunks / 2) * cdiv(D, 32);
+      embed_grad_heavy_kernel<TT, ACC><<<static_cast<unsigned>(std::min<int64_t>(most, int64_t(sms) * 8)), kEgWarps * 32,
+                                         0, s>>>(key, p.num_heavy, p.heavy, part, static_cast<TT*>(dtable), D, scale);
+      return launch_status();
+    };
+    using E1 = std::integral_constant<int, 1>;
+    using E8 = std::integral_constant<int, 8>;
+    if (acc) return vec ? run(E8{}, std::true_type{}) : run(E1{}, std::true_type{});
+    return vec ? run(E8{}, std::false_type{}) : run(E1{}, std::false_type{});
+  });
+}
+
+int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm, float* stats, void* ws,
+                 size_t ws_bytes, void* stream) {
+  if (num_tensors < 0 || !(max_norm >= 0.f) || !stats || !aligned_to(stats, 4) || (num_tensors > 0 && !tensors) || !ws ||
+      !aligned16(ws) || ws_bytes < bl_workspace_bytes(BL_OP_GRAD_CLIP, num_tensors, 0, 0))
+    return BL_ERR_INVALID_ARG;
+  try {
+    // outputs are buffers of their own, or exactly the gradient they scale
+    struct Range {
+      uintptr_t a, b;
+      int i;
+    };
+    std::vector<Range> outs;
+    outs.reserve(size_t(num_tensors));
+    int64_t total = 0;
+    for (int i = 0; i < num_tensors; ++i) {
+      const bl_grad_tensor& t = tensors[i];
+      if (!type_ok(t.type) || t.numel < 0) return BL_ERR_INVALID_ARG;
+      if (t.numel == 0) continue;
+      const int es = type_bytes(t.type);
+      if (!t.g || !aligned_to(t.g, es) || !aligned_to(t.out, es)) return BL_ERR_INVALID_ARG;
+      if (t.numel >= kMaxProduct || (total += t.numel) >= kMaxProduct) return BL_ERR_UNSUPPORTED;
+      const uintptr_t o = reinterpret_cast<uintptr_t>(t.out);
+      if (t.out) outs.push_back(Range{o, o + uintptr_t(t.numel) * uintptr_t(es), i});
+    }
+    std::sort(outs.begin(), outs.end(), [](const Range& l, const Range& r) { return l.a < r.a; });
+    for (size_t j = 1; j < outs.size(); ++j)
+      if (outs[j].a < outs[j - 1].b) return BL_ERR_INVALID_ARG;
+    for (int i = 0; i < num_tensors && !outs.empty(); ++i) {
+      const bl_grad_tensor& t = tensors[i];
+      if (t.numel == 0) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(t.g), b = a + uintptr_t(t.numel) * uintptr_t(type_bytes(t.type));
+      auto it = std::lower_bound(outs.begin(), outs.end(), b, [](const Range& l, uintptr_t v) { return l.a < v; });
+      if (it != outs.begin() && (it - 1)->b > a && ((it - 1)->a != a || (it - 1)->i != i)) return BL_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    const int rc = device_setup(&sms);
+    if (rc != BL_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    double* sums = static_cast<double*>(ws);
+    const int ctas = std::min(sms * 4, kGcMaxCtas);
+    static thread_local GcParams<kGcMaxTensors> P;
+    // launches of up to kGcMaxTensors tensors: all the norms, then all the products
+    int num_sums = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      int i = 0, launch = 0;
+      do {
+        P.n = 0;
+        int64_t chunks = 0;
+        bool writes = false;
+        for (; i < num_tensors && P.n < kGcMaxTensors; ++i) {
+          const bl_grad_tensor& t = tensors[i];
+          if (t.numel == 0) continue;
+          const int es = type_bytes(t.type);
+          P.t[P.n] = GcTensor{t.g, t.out, t.numel};
+          P.f32[P.n] = t.type == BL_TYPE_F32;
+          P.chunk0[P.n] = static_cast<int32_t>(chunks);
+          const int64_t mis = int64_t(reinterpret_cast<uintptr_t>(t.g) & 15u) / es;
+          chunks += cdiv(t.numel + mis, int64_t(kGcChunkVecs) * 16 / es);
+          writes |= t.out != nullptr;
+          ++P.n;
+        }
+        P.chunk0[P.n] = static_cast<int32_t>(chunks);
+        const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, ctas)));
+        if (pass == 0) {
+          grad_norm_kernel<kGcMaxTensors><<<grid, kGcThreads, 0, s>>>(P, sums + num_sums);
+          num_sums += grid;
+        } else if (writes || launch == 0) {
+          grad_scale_kernel<kGcMaxTensors><<<writes ? grid : 1, kGcThreads, 0, s>>>(P, sums, num_sums, max_norm,
+                                                                                    launch == 0 ? stats : nullptr);
+        }
+        ++launch;
+        const int st = launch_status();
+        if (st != BL_OK) return st;
+      } while (i < num_tensors);
+    }
+    return BL_OK;
+  } catch (...) {  // out of host memory
+    return BL_ERR_CUDA;
+  }
 }
 
 int bl_device_error(void* stream, int clear, int* where_out) {

@@ -37,6 +37,8 @@ enum : int {
   kWhereSsEpilogue = 10,
   kWhereMmaInbox = 11,  // the few-token warp-MMA GEMV
   kWhereStackRing = 12, // a layer-stack weight slot
+  kWhereEmbeddingId = 13,      // an id outside the table (lookup)
+  kWhereEmbeddingGradId = 14,  // an id outside the table (gradient)
 };
 
 // Bounded waits give up after this many nanoseconds of %globaltimer.

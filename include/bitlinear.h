@@ -69,6 +69,9 @@ extern "C" {
 #define BL_OP_W1A8_EX 6 /* bitlinear_w1a8_ex with a per-tensor quantiser */
 #define BL_OP_W1A16_STACK 7 /* bin_linear_w1a16_stack(_batch) (M tokens, N = total outputs; K ignored) */
 #define BL_OP_W1A16_BACKWARD 8 /* bin_linear_w1a16_backward */
+#define BL_OP_LAYER_NORM_BACKWARD 9 /* bl_layer_norm_backward (N ignored) */
+#define BL_OP_EMBEDDING_BACKWARD 10 /* bl_embedding_backward (M = T tokens, N = V rows, K = D columns) */
+#define BL_OP_GRAD_CLIP 11          /* bl_grad_clip (M = number of tensors; N and K ignored) */
 
 /* Library ABI version (this header: 1). */
 int bl_abi_version(void);
@@ -305,6 +308,108 @@ int bitlinear_w1a8_ex(const uint16_t* x, const uint32_t* packed, const float* be
  */
 int bin_xnor_gemm(const uint32_t* a, const uint32_t* b, int32_t* dot, int64_t M, int64_t N, int64_t K,
                   void* stream);
+
+/* ======================================================================
+ * Full-precision operators of a training step. Every linear of a binarized
+ * model but the head is binarized ("FBI-LLM" page); its embedding and its
+ * layer norms stay in full precision. Together with
+ * bin_linear_w1a16_backward these calls give the gradients of a model's
+ * trunk, and the norm over all of them.
+ *
+ * Where they differ from the conventions above: element types are arguments,
+ * any number of columns is taken, pointers need the alignment of their
+ * element only (16-byte aligned rows are read and written fastest), and rows
+ * may have a pitch (ld*, in elements) where one is named. Sums are fp32 or
+ * wider and each result is rounded to its type once. Results do not depend
+ * on the order of execution: the same call gives the same bits.
+ * ====================================================================== */
+#define BL_TYPE_BF16 0
+#define BL_TYPE_F32 1
+
+/*
+ * bl_layer_norm -- y_mk = (x_mk - mu_m) * rstd_m * weight_k + bias_k with
+ *   mu_m = mean_k x_mk,  rstd_m = 1 / sqrt(mean_k (x_mk - mu_m)^2 + eps).
+ * x [M x K] of x_type, y [M x K] of y_type, row pitches ldx, ldy >= K.
+ * weight and bias [K] fp32, each may be NULL (1 and 0). mean and rstd [M]
+ * fp32 receive the statistics for the backward pass; each may be NULL.
+ * eps > 0. K >= 1; M == 0 is a no-op. y may be x itself (same type, same
+ * pitch); otherwise they must not overlap.
+ */
+int bl_layer_norm(const void* x, int x_type, int64_t ldx, const float* weight, const float* bias, void* y, int y_type,
+                  int64_t ldy, float* mean, float* rstd, int64_t M, int64_t K, float eps, void* stream);
+
+/*
+ * bl_layer_norm_backward -- gradients of bl_layer_norm. With
+ * z_mk = (x_mk - mu_m) * rstd_m and g_mk = dy_mk * weight_k:
+ *   dx_mk      = rstd_m * (g_mk - mean_k g_mk - z_mk * mean_k (g_mk z_mk))
+ *   dweight_k  = sum_m dy_mk z_mk,   dbias_k = sum_m dy_mk        (fp32)
+ * x, weight, mean and rstd as in the forward pass (mean and rstd as it wrote
+ * them: a row's mean is corrected for their rounding). dy [M x K] of dy_type,
+ * dx [M x K] of x's type, pitches lddy, lddx >= K. dx, dweight and dbias may
+ * each be NULL (not computed). dx must be a buffer of its own. M == 0
+ * zero-fills dweight and dbias. ws: bl_workspace_bytes(
+ * BL_OP_LAYER_NORM_BACKWARD, M, 0, K) bytes, 16-byte aligned, needed for
+ * dweight or dbias (else it may be NULL).
+ */
+int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* weight, const float* mean,
+                           const float* rstd, const void* dy, int dy_type, int64_t lddy, void* dx, int64_t lddx,
+                           float* dweight, float* dbias, int64_t M, int64_t K, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * bl_embedding -- y_t = scale * table[ids_t], t = 0 .. T - 1.
+ * ids [T] of id_type, table [V x D] of table_type, y [T x D] of y_type, all
+ * dense; the product is taken in fp32. A token outside [0, V) gets a row of
+ * zeros, and BL_ERR_INVALID_ARG is recorded in the device error word
+ * (bl_device_error). T == 0 is a no-op. T, V < 2^31.
+ */
+#define BL_IDS_I32 0
+#define BL_IDS_I64 1
+int bl_embedding(const void* ids, int id_type, const void* table, int table_type, void* y, int y_type, int64_t T,
+                 int64_t V, int64_t D, float scale, void* stream);
+
+/*
+ * bl_embedding_backward -- the gradient of the whole table:
+ *   dtable_v = scale * sum_{t: ids_t = v} dy_t      (fp32 sums, in the order of t
+ *                                                    within runs of 32 sorted tokens)
+ * dy [T x D] of dy_type, dtable [V x D] of table_type. Rows that no token
+ * names are zero-filled. With BL_EMBED_ACCUMULATE the sums are added to
+ * dtable instead, and rows that no token names are not touched (a table that
+ * other gradients go to as well, or several batches). Tokens equal to
+ * padding_id (negative: none; otherwise < V) and tokens outside [0, V) give
+ * nothing; the latter are recorded in the device error word. T == 0
+ * zero-fills dtable (or does nothing with BL_EMBED_ACCUMULATE). ws:
+ * bl_workspace_bytes(BL_OP_EMBEDDING_BACKWARD, T, V, D) bytes, 16-byte
+ * aligned, not shared with a call still running.
+ */
+#define BL_EMBED_ACCUMULATE 1u
+int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_type, void* dtable, int table_type,
+                          int64_t T, int64_t V, int64_t D, float scale, int64_t padding_id, unsigned flags, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * bl_grad_clip -- the 2-norm over all elements of the given tensors, and the
+ * tensors scaled down to a largest norm:
+ *   norm = sqrt(sum g^2),  coef = min(1, max_norm / (norm + 1e-6)),  out = coef * g
+ * `tensors` is a HOST array (read during the call only). g and out: numel
+ * dense elements of `type`; out may be g (in place), a buffer of its own, or
+ * NULL (counted in the norm, not written). No out may overlap another out or
+ * another tensor's g (BL_ERR_INVALID_ARG): a tensor may not be listed twice
+ * in place. stats: two device floats, the norm (of the unscaled gradients;
+ * infinity above the largest float) and coef. Sums of squares are fp64, so
+ * the norm holds at any scale of g. A gradient that holds a NaN makes norm,
+ * coef and every out NaN; one that holds an infinity makes coef 0. Nothing
+ * is written in place where coef is 1. max_norm >= 0 (infinity: the norm
+ * alone). ws: bl_workspace_bytes(BL_OP_GRAD_CLIP, num_tensors, 0, 0) bytes,
+ * 16-byte aligned, not shared with a call still running.
+ */
+typedef struct bl_grad_tensor {
+  const void* g;
+  void* out;
+  int64_t numel;
+  int32_t type; /* BL_TYPE_BF16 or BL_TYPE_F32, of g and out */
+} bl_grad_tensor;
+int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm, float* stats, void* ws,
+                 size_t ws_bytes, void* stream);
 
 /*
  * bl_device_error -- synchronise `stream`, then return the first in-kernel
