@@ -1,7 +1,8 @@
 """Binarized linear layers on NVIDIA B200 (sm_100a).
 
-Thin ctypes binding over ``libbitlinear.so`` (C ABI in ``include/bitlinear.h``).
-Each function marshals torch tensors into device pointers and the current
+Thin binding over ``libbitlinear.so`` (C ABI in ``include/bitlinear.h``): ctypes,
+and for the short full-precision operators the native ``_native.so``. Each
+function marshals torch tensors into device pointers and the current
 CUDA stream and calls the entry point of the same name; every step of the
 computation runs in the library's CUDA kernels. There is no CPU fallback:
 if the library is missing, importing the binding raises.
@@ -24,12 +25,14 @@ if the library is missing, importing the binding raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libbitlinear.so")
+NATIVE_PATH = os.path.join(_PKG, "_native.so")
 
 BL_OK = 0
 BL_ERR_INVALID_ARG = -1
@@ -140,6 +143,19 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+def _load_native():
+    """The native binding of the full-precision operators (csrc/bl_binding.cpp)."""
+    if not os.path.exists(NATIVE_PATH):
+        raise ImportError(f"{NATIVE_PATH} is missing: build it with `python bit_linear_layers_b200/build.py`")
+    spec = importlib.util.spec_from_file_location("bit_linear_layers_b200._native", NATIVE_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+_native = _load_native()
 
 
 def status_string(status: int) -> str:
@@ -436,61 +452,8 @@ def bin_xnor_gemm(a: torch.Tensor, b: torch.Tensor, K: int, *, out=None):
 
 
 # ---- full-precision operators of a training step
-
-_TYPE = {torch.bfloat16: BL_TYPE_BF16, torch.float32: BL_TYPE_F32}
-_ID_TYPE = {torch.int32: BL_IDS_I32, torch.int64: BL_IDS_I64}
-
-
-def _call(name: str, device: torch.device, *args) -> None:
-    """Call an entry point on the current stream of `device`, with `device` current."""
-    if device.index == torch.cuda.current_device():
-        rc = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            rc = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
-    if rc != BL_OK:
-        raise BitLinearError(name, rc)
-
-
-def _typed(t: torch.Tensor, types: dict, name: str, device: torch.device) -> int:
-    """The BL_* code of t's element type; t has to be on `device`."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}" if device.type == "cuda"
-                         else f"{name} must be a CUDA tensor")
-    code = types.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in types)}, got {t.dtype}")
-    return code
-
-
-def _rows(t: torch.Tensor, M: int, K: int, name: str) -> int:
-    """Row pitch of an [M, K] tensor whose rows are dense."""
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != K:
-        raise ValueError(f"{name} must be [{M}, {K}], got {list(t.shape)}")
-    ld, s = t.stride()
-    if (s != 1 and K > 1) or (ld < K and M > 1):
-        raise ValueError(f"{name} must have dense rows that do not overlap")
-    return max(ld, K)
-
-
-def _dense(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, name: str, device: torch.device):
-    """Pointer of a dense tensor of that shape and type (None: none)."""
-    if t is None:
-        return None
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
-    return t.data_ptr()
-
-
-def _ws(op: int, M: int, N: int, K: int, device: torch.device, ws):
-    need = lib.bl_workspace_bytes(op, M, N, K)
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
-    return ws
+# The checks of arguments, the allocations and the calls are in csrc/bl_binding.cpp.
+_native.set_error(BitLinearError)
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
@@ -499,26 +462,9 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     pitch): y = (x - mu) / sqrt(var + eps) * weight + bias, with weight and
     bias fp32 [K] or None. y has out_dtype (default: x's) or is written to
     `out`, which may be x. With stats=True returns (y, mean, rstd), the fp32
-    [M] statistics that layer_norm_backward takes."""
-    dev = x.device
-    xt = _typed(x, _TYPE, "x", dev)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got {list(x.shape)}")
-    M, K = x.shape
-    ldx = _rows(x, M, K, "x")
-    if out is None:
-        out = torch.empty((M, K), dtype=out_dtype or x.dtype, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
-    yt, ldy = _typed(out, _TYPE, "out", dev), _rows(out, M, K, "out")
-    if stats:
-        mean = torch.empty(M, dtype=torch.float32, device=dev) if mean is None else mean
-        rstd = torch.empty(M, dtype=torch.float32, device=dev) if rstd is None else rstd
-    f32 = torch.float32
-    _call("bl_layer_norm", dev, x.data_ptr(), xt, ldx, _dense(weight, (K,), f32, "weight", dev),
-          _dense(bias, (K,), f32, "bias", dev), out.data_ptr(), yt, ldy, _dense(mean, (M,), f32, "mean", dev),
-          _dense(rstd, (M,), f32, "rstd", dev), M, K, eps)
-    return (out, mean, rstd) if stats else out
+    [M] statistics that layer_norm_backward takes; mean and rstd, where
+    given, receive them."""
+    return _native.layer_norm(x, weight, bias, eps, out, out_dtype, stats, mean, rstd)
 
 
 def layer_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor, rstd: torch.Tensor,
@@ -527,54 +473,14 @@ def layer_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, mean: torc
     """Gradients of layer_norm: returns (dx [M, K] of x's type or None,
     dweight [K] fp32 or None, dbias [K] fp32 or None). mean and rstd are the
     statistics the forward pass returned."""
-    dev = x.device
-    xt, gt = _typed(x, _TYPE, "x", dev), _typed(dy, _TYPE, "dy", dev)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got {list(x.shape)}")
-    M, K = x.shape
-    ldx, lddy = _rows(x, M, K, "x"), _rows(dy, M, K, "dy")
-    f32 = torch.float32
-    lddx = K
-    if not want_dx:
-        dx = None
-    elif dx is None:
-        dx = torch.empty((M, K), dtype=x.dtype, device=dev)
-    else:
-        if _typed(dx, _TYPE, "dx", dev) != xt:
-            raise ValueError(f"dx must be {x.dtype}, got {dx.dtype}")
-        lddx = _rows(dx, M, K, "dx")
-    if want_dw:
-        dweight = torch.empty(K, dtype=f32, device=dev) if dweight is None else dweight
-        dbias = torch.empty(K, dtype=f32, device=dev) if dbias is None else dbias
-        ws = _ws(BL_OP_LAYER_NORM_BACKWARD, M, 0, K, dev, ws)
-    else:
-        dweight = dbias = ws = None
-    _call("bl_layer_norm_backward", dev, x.data_ptr(), xt, ldx, _dense(weight, (K,), f32, "weight", dev),
-          _dense(mean, (M,), f32, "mean", dev), _dense(rstd, (M,), f32, "rstd", dev), dy.data_ptr(), gt, lddy,
-          None if dx is None else dx.data_ptr(), lddx, _dense(dweight, (K,), f32, "dweight", dev),
-          _dense(dbias, (K,), f32, "dbias", dev), M, K, None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel())
-    return dx, dweight, dbias
+    return _native.layer_norm_backward(x, weight, mean, rstd, dy, want_dx, want_dw, dx, dweight, dbias, ws)
 
 
 def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, out=None, out_dtype=None):
     """y = scale * table[ids]: ids int32 or int64 of any shape, table [V, D]
     bf16 or fp32; y [*ids.shape, D] of out_dtype (default: the table's). Ids
     outside [0, V) give rows of zeros and are recorded in device_error()."""
-    dev = table.device
-    it, tt = _typed(ids, _ID_TYPE, "ids", dev), _typed(table, _TYPE, "table", dev)
-    if table.dim() != 2 or not table.is_contiguous() or not ids.is_contiguous():
-        raise ValueError("table must be a contiguous [V, D] tensor and ids contiguous")
-    V, D = table.shape
-    shape = (*ids.shape, D)
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype or table.dtype, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
-    yt = _typed(out, _TYPE, "out", dev)
-    _call("bl_embedding", dev, ids.data_ptr(), it, table.data_ptr(), tt, _dense(out, shape, out.dtype, "out", dev), yt,
-          ids.numel(), V, D, scale)
-    return out
+    return _native.embedding(ids, table, scale, out, out_dtype)
 
 
 def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, V: int, *, scale: float = 1.0,
@@ -583,58 +489,7 @@ def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, V: int, *, scale: fl
     out_dtype (default: fp32), row v = scale * the sum of dy over the tokens
     that equal v, zeros elsewhere. With accumulate=True the sums are added to
     `out`. Tokens equal to padding_id give nothing."""
-    dev = dy.device
-    it, gt = _typed(ids, _ID_TYPE, "ids", dev), _typed(dy, _TYPE, "dy", dev)
-    D = dy.shape[-1] if dy.dim() else 0
-    if tuple(dy.shape) != (*ids.shape, D) or not dy.is_contiguous() or not ids.is_contiguous():
-        raise ValueError(f"dy must be a contiguous [*ids.shape, D] tensor and ids contiguous, got {list(dy.shape)} for "
-                         f"ids {list(ids.shape)}")
-    if padding_id is not None and not 0 <= padding_id < V:
-        raise ValueError(f"padding_id must be in [0, {V}), got {padding_id}")
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate=True adds to `out`: give it")
-        out = torch.empty((V, D), dtype=out_dtype or torch.float32, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
-    tt = _typed(out, _TYPE, "out", dev)
-    T = ids.numel()
-    ws = _ws(BL_OP_EMBEDDING_BACKWARD, T, V, D, dev, ws)
-    _call("bl_embedding_backward", dev, ids.data_ptr(), it, dy.data_ptr(), gt,
-          _dense(out, (V, D), out.dtype, "out", dev), tt, T, V, D, scale, -1 if padding_id is None else padding_id,
-          BL_EMBED_ACCUMULATE if accumulate else 0, ws.data_ptr(), ws.numel())
-    return out
-
-
-def _grad_clip(tensors, outs, max_norm, stats, ws):
-    n = len(tensors)
-    if n == 0:
-        raise ValueError("no tensors")
-    dev = tensors[0].device
-    if dev.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    rows = []
-    for t, o in zip(tensors, outs):
-        code = _TYPE.get(t.dtype)
-        if code is None or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"tensors must be contiguous bf16 or fp32 tensors on {dev}, got {t.dtype} {list(t.shape)} "
-                             f"on {t.device}")
-        numel = t.numel()
-        if o is t:
-            rows.append((t.data_ptr(), t.data_ptr(), numel, code))
-        elif o is None:
-            rows.append((t.data_ptr(), 0, numel, code))
-        else:
-            if o.dtype != t.dtype or o.device != dev or o.numel() != numel or not o.is_contiguous():
-                raise ValueError("an output must be a contiguous tensor of its gradient's type, size and device")
-            rows.append((t.data_ptr(), o.data_ptr(), numel, code))
-    table = (GradTensor * n)(*rows)
-    if stats is None:
-        stats = torch.empty(2, dtype=torch.float32, device=dev)
-    ws = _ws(BL_OP_GRAD_CLIP, n, 0, 0, dev, ws)
-    _call("bl_grad_clip", dev, ctypes.byref(table), n, max_norm, _dense(stats, (2,), torch.float32, "stats", dev),
-          ws.data_ptr(), ws.numel())
-    return stats[0], stats[1]
+    return _native.embedding_backward(ids, dy, V, scale, padding_id, out, out_dtype, accumulate, ws)
 
 
 def grad_clip(tensors, max_norm: float, *, out=None, stats=None, ws=None):
@@ -643,17 +498,12 @@ def grad_clip(tensors, max_norm: float, *, out=None, stats=None, ws=None):
     tensors of `out` (one for each; None: not written). Returns (norm, coef)
     as fp32 device scalars (the two elements of `stats`); nothing waits for
     the GPU. A NaN among the gradients makes everything NaN."""
-    tensors = list(tensors)
-    outs = tensors if out is None else list(out)
-    if len(outs) != len(tensors):
-        raise ValueError(f"{len(outs)} outputs for {len(tensors)} tensors")
-    return _grad_clip(tensors, outs, max_norm, stats, ws)
+    return _native.grad_clip(list(tensors), None if out is None else list(out), False, max_norm, stats, ws)
 
 
 def grad_norm(tensors, *, stats=None, ws=None):
     """The 2-norm over all elements of the tensors, as an fp32 device scalar."""
-    tensors = list(tensors)
-    return _grad_clip(tensors, [None] * len(tensors), float("inf"), stats, ws)[0]
+    return _native.grad_clip(list(tensors), None, True, float("inf"), stats, ws)[0]
 
 
 def device_error(clear: bool = True, device=None) -> tuple[int, int]:

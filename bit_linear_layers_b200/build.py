@@ -1,4 +1,5 @@
-"""Build ``libbitlinear.so`` in-tree for sm_100a with nvcc.
+"""Build ``libbitlinear.so`` in-tree for sm_100a with nvcc, and the native
+torch binding ``_native.so`` over it with the host compiler.
 
     python bit_linear_layers_b200/build.py [--verbose-ptxas]
 
@@ -14,6 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "bl_api.cu")
 LIB = os.path.join(PKG, "libbitlinear.so")
+BINDING_SRC = os.path.join(PKG, "csrc", "bl_binding.cpp")
+BINDING = os.path.join(PKG, "_native.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 NVCC_FLAGS = [
@@ -26,7 +29,7 @@ NVCC_FLAGS = [
 
 def sources():
     d = os.path.join(PKG, "csrc")
-    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh"))]
+    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh", ".cpp"))]
 
 
 def build(verbose_ptxas: bool = False, out: str = LIB) -> str:
@@ -35,13 +38,35 @@ def build(verbose_ptxas: bool = False, out: str = LIB) -> str:
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.run(cmd, check=True)
+    if out == LIB:
+        build_binding()
+    return out
+
+
+def build_binding(out: str = BINDING) -> str:
+    """The torch binding: links the C ABI library beside it and torch's own libraries."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(device_type="cuda")]
+    libs = cpp_extension.library_paths(device_type="cpu")
+    # the system's g++, whatever $CXX names: exceptions cross into torch's libraries, so both have to use the
+    # one shared libstdc++ (a compiler that links its own statically gives a binding that crashes on a refusal)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{p}" if p != INCLUDE else f"-I{p}" for p in inc), "-o", out, BINDING_SRC,
+           f"-L{PKG}", "-l:libbitlinear.so", *(f"-L{p}" for p in libs), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN", *(f"-Wl,-rpath,{p}" for p in libs)]
+    subprocess.run(cmd, check=True)
     return out
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = sources() + [os.path.join(INCLUDE, "bitlinear.h")]
     return any(os.path.getmtime(p) > t for p in deps)
 
