@@ -551,13 +551,13 @@ int check_norm_shape(int64_t M, int64_t K) {
 }
 
 struct NormWs {
-  int64_t parts;  // partial rows of dweight and dbias
+  int64_t parts;  // partial rows of dweight and of dbias there is room for
   size_t shift, part, bytes;
 };
 NormWs norm_ws(int64_t M, int64_t K) {
   NormWs w{};
   if (M < 1 || K < 1 || M > kMaxDim || K > kMaxDim || M >= kMaxProduct / K) return w;
-  w.parts = std::min<int64_t>(cdiv(M, 64), 128);
+  w.parts = std::min<int64_t>(M, K <= 1024 ? kNormMaxParts : kNormMaxParts / 2);
   w.shift = 0;
   w.part = align256(size_t(M) * 4);
   w.bytes = w.part + align256(size_t(2 * w.parts) * size_t(K) * 4);
@@ -591,6 +591,48 @@ EmbedWs embed_ws(int64_t T, int64_t V, int64_t D) {
 }
 
 inline int64_t gc_launches(int64_t n) { return n < 1 ? 1 : cdiv(n, kGcMaxTensors); }
+
+// rows of `type` that can be accessed eight elements at a time
+inline bool rows_vec(const void* p, int type, int64_t ld, int64_t K, int64_t M) {
+  return K % 8 == 0 && (M <= 1 || ld % 8 == 0) && aligned_to(p, 8 * type_bytes(type));
+}
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// The layer norms' tiling: f(E, NV, W) (elements per access, accesses per
+// thread, warps per row) of the smallest tile that holds a row, or `other`
+// where none does. Rows of up to 256 columns go to one warp each.
+template <int MAXK, typename F, typename O>
+int with_row_tile(bool vec, int64_t K, F&& f, O&& other) {
+  if (vec) {
+    if (K <= 256) return f(Int<8>{}, Int<1>{}, Int<1>{});
+    if (K <= 1024) return f(Int<8>{}, Int<1>{}, Int<4>{});
+    if (K <= 2048) return f(Int<8>{}, Int<1>{}, Int<8>{});
+    if (K <= 4096) return f(Int<8>{}, Int<2>{}, Int<8>{});
+    if (K <= 8192) return f(Int<8>{}, Int<2>{}, Int<16>{});
+    if constexpr (MAXK > 8192)
+      if (K <= 16384) return f(Int<8>{}, Int<4>{}, Int<16>{});
+  } else {
+    if (K <= 256) return f(Int<1>{}, Int<8>{}, Int<1>{});
+    if (K <= 1024) return f(Int<1>{}, Int<8>{}, Int<4>{});
+    if (K <= 4096) return f(Int<1>{}, Int<8>{}, Int<16>{});
+    if (K <= 8192) return f(Int<1>{}, Int<16>{}, Int<16>{});
+  }
+  return other();
+}
+
+// CTAs of a persistent kernel over `units`: as many as fit at once, evenly loaded
+template <typename Kernel>
+int64_t resident_ctas(Kernel k, int threads, int sms, int64_t units, int64_t most) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, 0) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  const int64_t cap = std::min<int64_t>(int64_t(n) * sms, most);
+  return units <= cap ? units : cdiv(units, cdiv(units, cap));
+}
 
 // f(uint16_t or float of `a`, of `b`)
 template <typename F>
@@ -1035,15 +1077,29 @@ int bl_layer_norm(const void* x, int x_type, int64_t ldx, const float* weight, c
       !aligned_to(bias, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return BL_ERR_INVALID_ARG;
   if (x == y && (x_type != y_type || ldx != ldy)) return BL_ERR_INVALID_ARG;
-  rc = device_setup(nullptr);
+  int sms = 0;
+  rc = device_setup(&sms);
   if (rc != BL_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return with_types(x_type, y_type, [&](auto tx, auto ty) {
     using TX = decltype(tx);
     using TY = decltype(ty);
-    layer_norm_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
-        static_cast<const TX*>(x), ldx, weight, bias, static_cast<TY*>(y), ldy, mean, rstd, K, eps);
-    return launch_status();
+    const bool v = rows_vec(x, x_type, ldx, K, M) && rows_vec(y, y_type, ldy, K, M);
+    return with_row_tile<16384>(
+        v, K,
+        [&](auto e, auto nv, auto warps) {
+          constexpr int E = decltype(e)::value, NV = decltype(nv)::value, W = decltype(warps)::value;
+          auto kernel = layer_norm_rows_kernel<TX, TY, E, NV, W>;
+          const int64_t grid = resident_ctas(kernel, row_threads(W), sms, cdiv(M, rows_per_cta(W)), kMaxDim);
+          kernel<<<static_cast<unsigned>(grid), row_threads(W), 0, s>>>(static_cast<const TX*>(x), ldx, weight, bias,
+                                                                       static_cast<TY*>(y), ldy, mean, rstd, M, int(K), eps);
+          return launch_status();
+        },
+        [&] {
+          layer_norm_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
+              static_cast<const TX*>(x), ldx, weight, bias, static_cast<TY*>(y), ldy, mean, rstd, K, eps);
+          return launch_status();
+        });
   });
 }
 
@@ -1076,23 +1132,45 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
   const NormWs w = norm_ws(M, K);
   if (w.bytes == 0) return BL_ERR_UNSUPPORTED;
   if (want_dw && (!ws || !aligned16(ws) || ws_bytes < w.bytes)) return BL_ERR_INVALID_ARG;
-  rc = device_setup(nullptr);
+  int sms = 0;
+  rc = device_setup(&sms);
   if (rc != BL_OK) return rc;
   float* shift = want_dw ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.shift) : nullptr;
   float* part = want_dw ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part) : nullptr;
   return with_types(x_type, dy_type, [&](auto tx, auto ty) {
     using TX = decltype(tx);
     using TY = decltype(ty);
-    layer_norm_dx_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
-        static_cast<const TX*>(x), ldx, weight, mean, rstd, static_cast<const TY*>(dy), lddy, static_cast<TX*>(dx),
-        lddx, shift, K);
-    int st = launch_status();
-    if (st != BL_OK || !want_dw) return st;
-    layer_norm_dw_kernel<TX, TY><<<dim3(unsigned(cdiv(K, 32)), unsigned(w.parts)), kNormThreads, 0, s>>>(
-        static_cast<const TX*>(x), ldx, mean, rstd, shift, static_cast<const TY*>(dy), lddy, part, M, K);
-    if ((st = launch_status()) != BL_OK) return st;
-    layer_norm_dw_sum_kernel<<<dim3(unsigned(cdiv(K, 32)), 2), kNormThreads, 0, s>>>(part, w.parts, K, dweight, dbias);
-    return launch_status();
+    const auto* xp = static_cast<const TX*>(x);
+    const auto* gp = static_cast<const TY*>(dy);
+    auto* dxp = static_cast<TX*>(dx);
+    auto sum_parts = [&](int64_t parts) {
+      layer_norm_dw_sum_kernel<<<dim3(unsigned(cdiv(K, 32)), 2), kNormThreads, 0, s>>>(part, parts, K, dweight, dbias);
+      return launch_status();
+    };
+    const bool v = rows_vec(x, x_type, ldx, K, M) && rows_vec(dy, dy_type, lddy, K, M) &&
+                   (!dx || rows_vec(dx, x_type, lddx, K, M));
+    return with_row_tile<8192>(
+        v, K,
+        [&](auto e, auto nv, auto warps) {
+          constexpr int E = decltype(e)::value, NV = decltype(nv)::value, W = decltype(warps)::value;
+          auto kernel = layer_norm_grad_rows_kernel<TX, TY, E, NV, W>;
+          const int64_t units = cdiv(M, rows_per_cta(W));
+          const int64_t grid = resident_ctas(kernel, row_threads(W), sms, units, want_dw ? w.parts : units);
+          kernel<<<static_cast<unsigned>(grid), row_threads(W), 0, s>>>(xp, ldx, weight, mean, rstd, gp, lddy, dxp, lddx,
+                                                                       part, M, int(K));
+          const int st = launch_status();
+          return st != BL_OK || !want_dw ? st : sum_parts(grid);
+        },
+        [&] {
+          layer_norm_dx_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(xp, ldx, weight, mean, rstd, gp,
+                                                                                       lddy, dxp, lddx, shift, K);
+          int st = launch_status();
+          if (st != BL_OK || !want_dw) return st;
+          const int64_t parts = std::min<int64_t>(cdiv(M, 64), 128);
+          layer_norm_dw_kernel<TX, TY><<<dim3(unsigned(cdiv(K, 32)), unsigned(parts)), kNormThreads, 0, s>>>(
+              xp, ldx, mean, rstd, shift, gp, lddy, part, M, K);
+          return (st = launch_status()) != BL_OK ? st : sum_parts(parts);
+        });
   });
 }
 
@@ -1110,7 +1188,7 @@ int bl_embedding(const void* ids, int id_type, const void* table, int table_type
   int rc = device_setup(nullptr);
   if (rc != BL_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool vec = D % 8 == 0 && aligned16(table) && aligned16(y);
+  const bool vec = rows_vec(table, table_type, D, D, 1) && rows_vec(y, y_type, D, D, 1);
   return with_types(table_type, y_type, [&](auto tt, auto ty) {
     using TT = decltype(tt);
     using TY = decltype(ty);
@@ -1120,8 +1198,8 @@ int bl_embedding(const void* ids, int id_type, const void* table, int table_type
           static_cast<const TI*>(ids), static_cast<const TT*>(table), static_cast<TY*>(y), T, V, D, scale);
       return launch_status();
     };
-    using E1 = std::integral_constant<int, 1>;
-    using E8 = std::integral_constant<int, 8>;
+    using E1 = Int<1>;
+    using E8 = Int<8>;
     if (id_type == BL_IDS_I64) return vec ? run(int64_t{}, E8{}) : run(int64_t{}, E1{});
     return vec ? run(int32_t{}, E8{}) : run(int32_t{}, E1{});
   });
@@ -1178,7 +1256,7 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
   const uint32_t* val = p.val[(passes + 1) & 1];
   const int64_t sum_blocks = cdiv(w.chunks * cdiv(D, kEgCols), kEgWarps);
   const int64_t zero_blocks = acc ? 0 : std::min<int64_t>(cdiv(V, kEgWarps), int64_t(sms) * 8);
-  const bool vec = D % 8 == 0 && aligned16(dy) && aligned16(dtable);
+  const bool vec = rows_vec(dy, dy_type, D, D, 1) && rows_vec(dtable, table_type, D, D, 1);
   return with_types(dy_type, table_type, [&](auto tg, auto tt) {
     using TG = decltype(tg);
     using TT = decltype(tt);
@@ -1195,8 +1273,8 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
                                          0, s>>>(key, p.num_heavy, p.heavy, part, static_cast<TT*>(dtable), D, scale);
       return launch_status();
     };
-    using E1 = std::integral_constant<int, 1>;
-    using E8 = std::integral_constant<int, 8>;
+    using E1 = Int<1>;
+    using E8 = Int<8>;
     if (acc) return vec ? run(E8{}, std::true_type{}) : run(E1{}, std::true_type{});
     return vec ? run(E8{}, std::false_type{}) : run(E1{}, std::false_type{});
   });

@@ -21,14 +21,106 @@ namespace bl {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kNormMaxParts = 148 * 8;  // partial rows of dweight and dbias
 
-// One CTA per row, three passes over the row (the later ones from L1/L2).
+// Rows in registers. W warps share a row; each of their threads holds NV
+// accesses of E elements of it, and the weight and bias of its columns for all
+// rows it meets (read again for each row they would cost more L2 traffic than
+// the row itself). CTAs stay and take rows in turn, the next row's loads in
+// flight while this one is reduced. W = 1: eight rows per CTA, no barriers.
+constexpr int rows_per_cta(int W) { return W == 1 ? 8 : 1; }
+constexpr int row_threads(int W) { return W == 1 ? 256 : W * 32; }
+
+template <typename TX, typename TY, int E, int NV, int W>
+__global__ void __launch_bounds__(row_threads(W))
+    layer_norm_rows_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w,
+                           const float* __restrict__ b, TY* __restrict__ y, int64_t ldy, float* __restrict__ mean,
+                           float* __restrict__ rstd, int64_t M, int K, float eps) {
+  __shared__ float sh[3 * W];
+  constexpr int RPC = rows_per_cta(W);
+  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * RPC;
+  int64_t m = static_cast<int64_t>(blockIdx.x) * RPC + (W == 1 ? threadIdx.x >> 5 : 0);
+  Raw<TX, E> cur[NV], nxt[NV];
+  auto fetch = [&](Raw<TX, E>(&r)[NV], int64_t row) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int k = (tid + u * W * 32) * E;
+      if (k < K)
+        r[u].load(x + row * ldx + k);
+      else
+        r[u].zero();
+    }
+  };
+  if (m < M) fetch(cur, m);
+  float wr[NV][E], br[NV][E];
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int k = (tid + u * W * 32) * E + j;
+      wr[u][j] = w && k < K ? w[k] : 1.f;
+      br[u][j] = b && k < K ? b[k] : 0.f;
+    }
+  const float inv_k = 1.0f / static_cast<float>(K);
+  for (; m < M; m += step) {
+    if (m + step < M) fetch(nxt, m + step);
+    float f[E];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      cur[u].get(f);
+      s[0] += tree_sum<E>(f);
+    }
+    block_sums<W>(s, sh);
+    const float c = s[0] * inv_k;
+    float q[2] = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if ((tid + u * W * 32) * E < K) {
+        cur[u].get(f);
+        float d2[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          f[j] -= c;
+          d2[j] = f[j] * f[j];
+        }
+        q[0] += tree_sum<E>(f);
+        q[1] += tree_sum<E>(d2);
+      }
+    }
+    block_sums<W>(q, sh + W);
+    const float md = q[0] * inv_k;
+    float var = q[1] * inv_k - md * md;
+    var = var < 0.f ? 0.f : var;  // a rounding below zero; NaN stays NaN
+    const float r = 1.0f / sqrtf(var + eps);
+    if (tid == 0) {
+      if (mean) mean[m] = c + md;
+      if (rstd) rstd[m] = r;
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int k = (tid + u * W * 32) * E;
+      if (k < K) {
+        cur[u].get(f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[j] = fmaf(((f[j] - c) - md) * r, wr[u][j], br[u][j]);
+        Elem<TY, E>::store(y + m * ldy + k, f);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) cur[u] = nxt[u];
+  }
+}
+
+// Rows too long for that: one CTA per row, three passes over the row (the
+// later ones from L1/L2).
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w, const float* __restrict__ b,
                       TY* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t K,
                       float eps) {
-  __shared__ float sh[2 * kNormWarps];
+  __shared__ float sh[3 * kNormWarps];
   const int64_t m = blockIdx.x;
   const TX* xr = x + m * ldx;
   TY* yr = y + m * ldy;
@@ -48,7 +140,7 @@ __global__ void __launch_bounds__(kNormThreads)
     q[0] += d;
     q[1] = fmaf(d, d, q[1]);
   }
-  block_sums<kNormWarps>(q, sh);
+  block_sums<kNormWarps>(q, sh + kNormWarps);
   const float md = q[0] * inv_k;
   float var = q[1] * inv_k - md * md;
   var = var < 0.f ? 0.f : var;  // a rounding below zero; NaN stays NaN
@@ -66,7 +158,137 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
-// One CTA per row: dx (where wanted) and the row's correction of the kept mean.
+// The gradient, rows in registers as in the forward pass: one pass over x and
+// dy gives dx, and each thread adds up dy z and dy of its columns over its rows;
+// a CTA ends with one partial row of both, which the kernel below adds up in
+// order. The mean is corrected as in the forward pass: md = mean (x - kept mean).
+template <typename TX, typename TG, int E, int NV, int W>
+__global__ void __launch_bounds__(row_threads(W))
+    layer_norm_grad_rows_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w,
+                                const float* __restrict__ mean, const float* __restrict__ rstd,
+                                const TG* __restrict__ dy, int64_t lddy, TX* __restrict__ dx, int64_t lddx,
+                                float* __restrict__ part, int64_t M, int K) {
+  __shared__ float sh[2][3 * W];
+  constexpr int RPC = rows_per_cta(W);
+  const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * RPC;
+  int64_t m = static_cast<int64_t>(blockIdx.x) * RPC + (W == 1 ? threadIdx.x >> 5 : 0);
+  Raw<TX, E> cx[NV], nx[NV];
+  Raw<TG, E> cg[NV], ng[NV];
+  auto fetch = [&](Raw<TX, E>(&rx)[NV], Raw<TG, E>(&rg)[NV], int64_t row) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int k = (tid + u * W * 32) * E;
+      if (k < K) {
+        rx[u].load(x + row * ldx + k);
+        rg[u].load(dy + row * lddy + k);
+      } else {
+        rx[u].zero();
+        rg[u].zero();
+      }
+    }
+  };
+  if (m < M) fetch(cx, cg, m);
+  float wr[NV][E], aw[NV][E], ab[NV][E];
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int k = (tid + u * W * 32) * E + j;
+      wr[u][j] = w && k < K ? w[k] : 1.f;
+      aw[u][j] = ab[u][j] = 0.f;
+    }
+  const float inv_k = 1.0f / static_cast<float>(K);
+  int buf = 0;
+  for (; m < M; m += step) {
+    const float c = mean[m], r = rstd[m];
+    if (m + step < M) fetch(nx, ng, m + step);
+    float fx[E], fg[E];
+    float s[3] = {0.f, 0.f, 0.f};  // sums of d, g and g d
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if ((tid + u * W * 32) * E < K) {
+        cx[u].get(fx);
+        cg[u].get(fg);
+        float gd[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          fx[j] -= c;
+          fg[j] *= wr[u][j];
+          gd[j] = fx[j] * fg[j];
+        }
+        s[0] += tree_sum<E>(fx);
+        s[1] += tree_sum<E>(fg);
+        s[2] += tree_sum<E>(gd);
+      }
+    }
+    block_sums<W>(s, sh[buf]);
+    buf ^= 1;
+    const float md = s[0] * inv_k, mg = s[1] * inv_k, mgz = r * (s[2] - md * s[1]) * inv_k;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int k = (tid + u * W * 32) * E;
+      if (k < K) {
+        cx[u].get(fx);
+        cg[u].get(fg);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const float z = ((fx[j] - c) - md) * r;
+          aw[u][j] = fmaf(fg[j], z, aw[u][j]);
+          ab[u][j] += fg[j];
+          fx[j] = r * (fmaf(fg[j], wr[u][j], -mg) - z * mgz);
+        }
+        if (dx) Elem<TX, E>::store(dx + m * lddx + k, fx);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      cx[u] = nx[u];
+      cg[u] = ng[u];
+    }
+  }
+  if (!part) return;
+  // partial rows: [0, P) dweight, [P, 2P) dbias
+  float* pw = part + static_cast<int64_t>(blockIdx.x) * K;
+  float* pb = pw + static_cast<int64_t>(gridDim.x) * K;
+  if constexpr (W == 1) {
+    constexpr int COLS = 32 * E * NV;
+    __shared__ float acc[8][2][COLS];
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        acc[warp][0][(tid + u * 32) * E + j] = aw[u][j];
+        acc[warp][1][(tid + u * 32) * E + j] = ab[u][j];
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * COLS; i += 256) {
+      const int k = i % COLS;
+      if (k < K) {
+        float t = acc[0][i / COLS][k];
+#pragma unroll
+        for (int v = 1; v < 8; ++v) t += acc[v][i / COLS][k];
+        (i < COLS ? pw : pb)[k] = t;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int k = (tid + u * W * 32) * E;
+      if (k < K) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          pw[k + j] = aw[u][j];
+          pb[k + j] = ab[u][j];
+        }
+      }
+    }
+  }
+}
+
+// Rows too long for that: dx and the weight's gradient separately, from two
+// readings of x and dy. One CTA per row: dx (where wanted) and the row's correction of the kept mean.
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_dx_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w,
