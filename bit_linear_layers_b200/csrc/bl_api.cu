@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cmath>
 #include <cstring>
@@ -600,38 +601,81 @@ inline bool rows_vec(const void* p, int type, int64_t ld, int64_t K, int64_t M) 
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// The layer norms' tiling: f(E, NV, W) (elements per access, accesses per
-// thread, warps per row) of the smallest tile that holds a row, or `other`
-// where none does. Rows of up to 256 columns go to one warp each.
-template <int MAXK, typename F, typename O>
-int with_row_tile(bool vec, int64_t K, F&& f, O&& other) {
-  if (vec) {
-    if (K <= 256) return f(Int<8>{}, Int<1>{}, Int<1>{});
-    if (K <= 1024) return f(Int<8>{}, Int<1>{}, Int<4>{});
-    if (K <= 2048) return f(Int<8>{}, Int<1>{}, Int<8>{});
-    if (K <= 4096) return f(Int<8>{}, Int<2>{}, Int<8>{});
-    if (K <= 8192) return f(Int<8>{}, Int<2>{}, Int<16>{});
-    if constexpr (MAXK > 8192)
-      if (K <= 16384) return f(Int<8>{}, Int<4>{}, Int<16>{});
-  } else {
-    if (K <= 256) return f(Int<1>{}, Int<8>{}, Int<1>{});
-    if (K <= 1024) return f(Int<1>{}, Int<8>{}, Int<4>{});
-    if (K <= 4096) return f(Int<1>{}, Int<8>{}, Int<16>{});
-    if (K <= 8192) return f(Int<1>{}, Int<16>{}, Int<16>{});
+// rows that `elems` elements at a time can be read or written of
+inline bool rows_aligned(const void* p, int type, int64_t ld, int64_t K, int64_t M, int elems) {
+  return K % elems == 0 && (M <= 1 || ld % elems == 0) && aligned_to(p, elems * type_bytes(type));
+}
+// rows whose 16-byte pieces can be copied whole
+inline bool rows_in_pieces(const void* p, int type, int64_t ld, int64_t K, int64_t M) {
+  return rows_aligned(p, type, ld, K, M, 16 / type_bytes(type));
+}
+
+// The layer norm's tiling: f(CPT, W) (columns per thread, warps per row) of the
+// smallest tile that holds a row. One warp per row up to 4096 columns, unless the
+// rows are so few (`few`) that spreading each over a CTA is what fills the GPU.
+template <typename F>
+int with_norm_tile(int64_t K, bool few, F&& f) {
+  if (few) {
+    if (K <= 1024) return f(Int<8>{}, Int<4>{});
+    if (K <= 4096) return f(Int<16>{}, Int<8>{});
+    if (K <= 8192) return f(Int<16>{}, Int<16>{});
   }
-  return other();
+  if (K <= 256) return f(Int<8>{}, Int<1>{});
+  if (K <= 512) return f(Int<16>{}, Int<1>{});
+  if (K <= 1024) return f(Int<32>{}, Int<1>{});
+  if (K <= 2048) return f(Int<64>{}, Int<1>{});
+  if (K <= 4096) return f(Int<128>{}, Int<1>{});
+  if (K <= 8192) return f(Int<64>{}, Int<4>{});
+  return f(Int<32>{}, Int<16>{});
+}
+
+// CTAs per SM of a kernel on the current device, looked up once per device
+// (and its dynamic shared memory allowed)
+template <auto Kernel>
+int ctas_per_sm(int threads, int smem) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return 0;
+  }
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if ((smem > 0 && !set_smem(Kernel, smem)) ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, size_t(smem)) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 // CTAs of a persistent kernel over `units`: as many as fit at once, evenly loaded
-template <typename Kernel>
-int64_t resident_ctas(Kernel k, int threads, int sms, int64_t units, int64_t most) {
-  int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, 0) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    n = 1;
-  }
-  const int64_t cap = std::min<int64_t>(int64_t(n) * sms, most);
+inline int64_t persistent_grid(int ctas_per_sm, int sms, int64_t units, int64_t most) {
+  const int64_t cap = std::min<int64_t>(int64_t(ctas_per_sm) * sms, most);
   return units <= cap ? units : cdiv(units, cdiv(units, cap));
+}
+
+// launch with programmatic serialisation: the kernel may be scheduled while
+// the one before it runs, and waits for it by itself
+template <typename... Params, typename... Args>
+int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return BL_ERR_CUDA;
+  }
+  return launch_status();
 }
 
 // f(uint16_t or float of `a`, of `b`)
@@ -1084,22 +1128,29 @@ int bl_layer_norm(const void* x, int x_type, int64_t ldx, const float* weight, c
   return with_types(x_type, y_type, [&](auto tx, auto ty) {
     using TX = decltype(tx);
     using TY = decltype(ty);
-    const bool v = rows_vec(x, x_type, ldx, K, M) && rows_vec(y, y_type, ldy, K, M);
-    return with_row_tile<16384>(
-        v, K,
-        [&](auto e, auto nv, auto warps) {
-          constexpr int E = decltype(e)::value, NV = decltype(nv)::value, W = decltype(warps)::value;
-          auto kernel = layer_norm_rows_kernel<TX, TY, E, NV, W>;
-          const int64_t grid = resident_ctas(kernel, row_threads(W), sms, cdiv(M, rows_per_cta(W)), kMaxDim);
-          kernel<<<static_cast<unsigned>(grid), row_threads(W), 0, s>>>(static_cast<const TX*>(x), ldx, weight, bias,
-                                                                       static_cast<TY*>(y), ldy, mean, rstd, M, int(K), eps);
-          return launch_status();
-        },
-        [&] {
-          layer_norm_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
-              static_cast<const TX*>(x), ldx, weight, bias, static_cast<TY*>(y), ldy, mean, rstd, K, eps);
-          return launch_status();
-        });
+    if (K > kNormMaxK) {
+      layer_norm_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
+          static_cast<const TX*>(x), ldx, weight, bias, static_cast<TY*>(y), ldy, mean, rstd, K, eps);
+      return launch_status();
+    }
+    constexpr int WIDE = 16 / int(sizeof(TX));
+    const bool wide = rows_aligned(x, x_type, ldx, K, M, WIDE) && rows_aligned(y, y_type, ldy, K, M, WIDE);
+    return with_norm_tile(K, M <= 2 * int64_t(sms), [&](auto cpt, auto warps) {
+      auto run = [&](auto e) {
+        constexpr int E = decltype(e)::value, CPT = decltype(cpt)::value, W = decltype(warps)::value;
+        using C = NormCfg<TX, E, CPT, W>;
+        constexpr auto kernel = layer_norm_rows_kernel<TX, TY, E, CPT, W>;
+        const int groups = int(std::min<int64_t>(C::GROUPS, cdiv(M, sms)));
+        // with fewer groups more CTAs fit, but then there are no rows for them
+        const int n = ctas_per_sm<kernel>(C::GROUPS * W * 32, C::smem(C::GROUPS));
+        if (n < 1) return int(BL_ERR_CUDA);
+        const int64_t grid = persistent_grid(n, sms, cdiv(M, groups), kMaxDim);
+        kernel<<<static_cast<unsigned>(grid), groups * W * 32, C::smem(groups), s>>>(
+            static_cast<const TX*>(x), ldx, weight, bias, static_cast<TY*>(y), ldy, mean, rstd, M, int(K), eps);
+        return launch_status();
+      };
+      return wide ? run(Int<WIDE>{}) : run(Int<1>{});
+    });
   });
 }
 
@@ -1144,33 +1195,52 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
     const auto* gp = static_cast<const TY*>(dy);
     auto* dxp = static_cast<TX*>(dx);
     auto sum_parts = [&](int64_t parts) {
-      layer_norm_dw_sum_kernel<<<dim3(unsigned(cdiv(K, 32)), 2), kNormThreads, 0, s>>>(part, parts, K, dweight, dbias);
-      return launch_status();
+      return launch_after(layer_norm_dw_sum_kernel, dim3(unsigned(cdiv(K, 32)), 2), kNormSumThreads, 0, s,
+                          static_cast<const float*>(part), int(parts), K, dweight, dbias);
     };
-    const bool v = rows_vec(x, x_type, ldx, K, M) && rows_vec(dy, dy_type, lddy, K, M) &&
-                   (!dx || rows_vec(dx, x_type, lddx, K, M));
-    return with_row_tile<8192>(
-        v, K,
-        [&](auto e, auto nv, auto warps) {
-          constexpr int E = decltype(e)::value, NV = decltype(nv)::value, W = decltype(warps)::value;
-          auto kernel = layer_norm_grad_rows_kernel<TX, TY, E, NV, W>;
-          const int64_t units = cdiv(M, rows_per_cta(W));
-          const int64_t grid = resident_ctas(kernel, row_threads(W), sms, units, want_dw ? w.parts : units);
-          kernel<<<static_cast<unsigned>(grid), row_threads(W), 0, s>>>(xp, ldx, weight, mean, rstd, gp, lddy, dxp, lddx,
-                                                                       part, M, int(K));
-          const int st = launch_status();
-          return st != BL_OK || !want_dw ? st : sum_parts(grid);
-        },
-        [&] {
-          layer_norm_dx_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(xp, ldx, weight, mean, rstd, gp,
-                                                                                       lddy, dxp, lddx, shift, K);
-          int st = launch_status();
-          if (st != BL_OK || !want_dw) return st;
-          const int64_t parts = std::min<int64_t>(cdiv(M, 64), 128);
-          layer_norm_dw_kernel<TX, TY><<<dim3(unsigned(cdiv(K, 32)), unsigned(parts)), kNormThreads, 0, s>>>(
-              xp, ldx, mean, rstd, shift, gp, lddy, part, M, K);
-          return (st = launch_status()) != BL_OK ? st : sum_parts(parts);
-        });
+    if (K > kNormGradMaxK) {
+      layer_norm_dx_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(xp, ldx, weight, mean, rstd, gp, lddy,
+                                                                                   dxp, lddx, shift, K);
+      int st = launch_status();
+      if (st != BL_OK || !want_dw) return st;
+      const int64_t parts = std::min<int64_t>(cdiv(M, 64), 128);
+      layer_norm_dw_kernel<TX, TY><<<dim3(unsigned(cdiv(K, 32)), unsigned(parts)), kNormThreads, 0, s>>>(
+          xp, ldx, mean, rstd, shift, gp, lddy, part, M, K);
+      return (st = launch_status()) != BL_OK ? st : sum_parts(parts);
+    }
+    auto launch = [&](auto kernel, int ctas, int threads, int smem, int64_t units) {
+      if (ctas < 1) return int(BL_ERR_CUDA);
+      const int64_t grid = persistent_grid(ctas, sms, units, want_dw ? w.parts : units);
+      kernel<<<static_cast<unsigned>(grid), threads, smem, s>>>(xp, ldx, weight, mean, rstd, gp, lddy, dxp, lddx, part, M,
+                                                                int(K));
+      const int st = launch_status();
+      return st != BL_OK || !want_dw ? st : sum_parts(grid);
+    };
+    constexpr int WIDE = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
+    const bool wide = rows_in_pieces(x, x_type, ldx, K, M) && rows_in_pieces(dy, dy_type, lddy, K, M) &&
+                      (!dx || rows_in_pieces(dx, x_type, lddx, K, M));
+    auto by_width = [&](auto e) {
+      constexpr int E = decltype(e)::value;
+      auto rows = [&](auto cpt) {
+        constexpr int CPT = decltype(cpt)::value;
+        using C = NormGradRowCfg<TX, TY, E, CPT>;
+        constexpr auto kernel = layer_norm_grad_rows_kernel<TX, TY, E, CPT>;
+        return launch(kernel, ctas_per_sm<kernel>(C::WARPS * 32, C::SMEM), C::WARPS * 32, C::SMEM, cdiv(M, C::WARPS));
+      };
+      auto tiles = [&](auto cpt, auto warps) {
+        constexpr int CPT = decltype(cpt)::value, W = decltype(warps)::value;
+        using C = NormGradTileCfg<TX, TY, E, CPT, W>;
+        constexpr auto kernel = layer_norm_grad_tile_kernel<TX, TY, E, CPT, W>;
+        return launch(kernel, ctas_per_sm<kernel>(C::THREADS, C::SMEM), C::THREADS, C::SMEM, cdiv(M, C::R));
+      };
+      if (K <= 256) return rows(Int<8>{});
+      if (K <= 512) return rows(Int<16>{});
+      if (K <= 1024) return tiles(Int<8>{}, Int<4>{});
+      if (K <= 2048) return tiles(Int<8>{}, Int<8>{});
+      if (K <= 4096) return tiles(Int<8>{}, Int<16>{});
+      return tiles(Int<16>{}, Int<16>{});
+    };
+    return wide ? by_width(Int<WIDE>{}) : by_width(Int<1>{});
   });
 }
 
