@@ -23,7 +23,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC,-Wall", "-shared",
-    "--expt-relaxed-constexpr", "--split-compile=0",
+    "--expt-relaxed-constexpr",
 ]
 
 

@@ -611,22 +611,24 @@ inline bool rows_in_pieces(const void* p, int type, int64_t ld, int64_t K, int64
 }
 
 // The layer norm's tiling: f(CPT, W) (columns per thread, warps per row) of the
-// smallest tile that holds a row. One warp per row up to 4096 columns, unless the
+// smallest tile that holds a row. 32 columns per thread where they are read many
+// at a time, fewer where they are read one by one (`wide` false) or where the
 // rows are so few (`few`) that spreading each over a CTA is what fills the GPU.
 template <typename F>
-int with_norm_tile(int64_t K, bool few, F&& f) {
-  if (few) {
+int with_norm_tile(int64_t K, bool wide, bool few, F&& f) {
+  if (K <= 256 && !few) return f(Int<8>{}, Int<1>{});
+  if (K > 8192) return f(Int<32>{}, Int<16>{});
+  if (few || !wide) {
     if (K <= 1024) return f(Int<8>{}, Int<4>{});
+    if (K <= 2048) return f(Int<16>{}, Int<4>{});
     if (K <= 4096) return f(Int<16>{}, Int<8>{});
-    if (K <= 8192) return f(Int<16>{}, Int<16>{});
+    return f(Int<16>{}, Int<16>{});
   }
-  if (K <= 256) return f(Int<8>{}, Int<1>{});
   if (K <= 512) return f(Int<16>{}, Int<1>{});
   if (K <= 1024) return f(Int<32>{}, Int<1>{});
-  if (K <= 2048) return f(Int<64>{}, Int<1>{});
-  if (K <= 4096) return f(Int<128>{}, Int<1>{});
-  if (K <= 8192) return f(Int<64>{}, Int<4>{});
-  return f(Int<32>{}, Int<16>{});
+  if (K <= 2048) return f(Int<32>{}, Int<2>{});
+  if (K <= 4096) return f(Int<32>{}, Int<4>{});
+  return f(Int<32>{}, Int<8>{});
 }
 
 // CTAs per SM of a kernel on the current device, looked up once per device
@@ -1135,7 +1137,7 @@ int bl_layer_norm(const void* x, int x_type, int64_t ldx, const float* weight, c
     }
     constexpr int WIDE = 16 / int(sizeof(TX));
     const bool wide = rows_aligned(x, x_type, ldx, K, M, WIDE) && rows_aligned(y, y_type, ldy, K, M, WIDE);
-    return with_norm_tile(K, M <= 2 * int64_t(sms), [&](auto cpt, auto warps) {
+    return with_norm_tile(K, wide, M <= 2 * int64_t(sms), [&](auto cpt, auto warps) {
       auto run = [&](auto e) {
         constexpr int E = decltype(e)::value, CPT = decltype(cpt)::value, W = decltype(warps)::value;
         using C = NormCfg<TX, E, CPT, W>;
@@ -1238,7 +1240,7 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
       if (K <= 1024) return tiles(Int<8>{}, Int<4>{});
       if (K <= 2048) return tiles(Int<8>{}, Int<8>{});
       if (K <= 4096) return tiles(Int<8>{}, Int<16>{});
-      return tiles(Int<16>{}, Int<16>{});
+      return tiles(Int<32>{}, Int<8>{});
     };
     return wide ? by_width(Int<WIDE>{}) : by_width(Int<1>{});
   });

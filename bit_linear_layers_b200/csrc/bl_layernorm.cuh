@@ -42,10 +42,11 @@ struct NormCfg {
   // fp32 rows of 16384 leave no room for them: read from L2 with each row
   static constexpr bool WB_MEM = SLOT > 48 * 1024, WB_SMEM = CPT > 16 && !WB_MEM;
   static constexpr int WB = WB_SMEM ? 8 * KP : 0;
-  // groups per CTA: two CTAs per SM where each holds at least four rows
+  // groups per CTA: up to 16 warps, two CTAs per SM where that takes no more than half of them away
   static constexpr int fit(int kb) { return (kb * 1024 - WB) / (S * SLOT); }
   static constexpr int least(int a, int b) { return a < b ? a : b; }
-  static constexpr int GROUPS = W > 1 ? least(fit(226), W >= 8 ? 1 : 4) : least(8, fit(112) >= 4 ? fit(112) : fit(226));
+  static constexpr int MOST = W == 1 ? 8 : 16 / W;
+  static constexpr int GROUPS = least(MOST, fit(112) >= (MOST + 1) / 2 ? fit(112) : fit(226));
   static constexpr int smem(int groups) { return WB + groups * S * SLOT; }
 };
 
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(512)
   using Row = StagedRow<TX, E>;
   constexpr int PAIRS = Row::PAIRS, UNIT = E == 1 ? 2 : E, NU = CPT / UNIT, T = W * 32, S = C::S;
   constexpr bool WB_REGS = !C::WB_SMEM && !C::WB_MEM;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float sh[16][3 * W];
   const int groups = blockDim.x / T, group = threadIdx.x / T, tid = threadIdx.x % T, warp = tid >> 5;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(512)
     Row::get(row, k, T, f);
     if constexpr (E == 1) f[0] = make_float2(k < K ? f[0].x : fill, k + T < K ? f[0].y : fill);
   };
-  constexpr bool HOLD = NU * UNIT <= 16;  // few columns: read once, held
+  constexpr bool HOLD = CPT <= 32;  // few columns: read and unpacked once, held
   for (; m < M; m += step, xr += step * ldx, yr += step * ldy) {
     cp_async_wait<S - 2>();
     group_sync<W>(1 + group);  // the whole row has arrived; the slot of the row before is free
@@ -152,10 +153,10 @@ __global__ void __launch_bounds__(512)
     float s[1] = {acc.x + acc.y};
     group_sums<W>(s, sh[group], warp, 1 + group);
     const float c = s[0] * inv_k;
-    float2 a1 = both(0.f), a2 = both(0.f);
+    float2 a1 = both(0.f), a2[2] = {both(0.f), both(0.f)};
 #pragma unroll 8
     for (int u = 0; u < NU; ++u) {
-      float2 f[PAIRS], d2[PAIRS];
+      float2 f[PAIRS];
       if constexpr (HOLD) {
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) f[j] = held[u][j];
@@ -169,12 +170,12 @@ __global__ void __launch_bounds__(512)
       for (int j = 0; j < PAIRS; ++j) {
         f[j] = add2(f[j], cu);
         if constexpr (HOLD) held[u][j] = f[j];
-        d2[j] = mul2(f[j], f[j]);
+        a2[j & 1] = fma2(f[j], f[j], a2[j & 1]);
       }
       a1 = add2(a1, tree_sum2<PAIRS>(f));
-      a2 = add2(a2, tree_sum2<PAIRS>(d2));
     }
-    float q[2] = {a1.x + a1.y, a2.x + a2.y};
+    a2[0] = add2(a2[0], a2[1]);
+    float q[2] = {a1.x + a1.y, a2[0].x + a2[0].y};
     group_sums<W>(q, sh[group] + W, warp, 1 + group);
     const float md = q[0] * inv_k;
     float var = q[1] * inv_k - md * md;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(256)
   using RowX = StagedRow<TX, E>;
   using RowG = StagedRow<TG, E>;
   constexpr int PAIRS = RowX::PAIRS, UNIT = E == 1 ? 2 : E, NU = CPT / UNIT, S = C::S;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = static_cast<int64_t>(gridDim.x) * C::WARPS;
   int64_t m = static_cast<int64_t>(blockIdx.x) * C::WARPS + warp;
@@ -401,27 +402,27 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// More columns: a CTA of W warps takes R rows at a time. First the rows' sums, W / R
-// warps to a row; then, each thread holding CPT columns, dx and the columns'
-// sums for all R rows. The sums of the next tile are formed before the
-// columns of this one, so that one barrier per tile serves both, and the tile
-// after that is on its way. (With the columns' threads also forming the row's
-// sums, every warp spent 15 shuffles and a barrier on each row, as much as on its
-// 8 columns.)
+// More columns: a CTA of W warps takes tiles of R rows, two on chip, one of them
+// on its way. First the rows' sums, each warp whole rows (or a share of one);
+// then, each thread holding CPT columns, dx and the columns' sums for all R rows.
+// What a tile costs beside its elements (the sums' shuffles, the copies'
+// addresses, the rows' constants) is paid per warp, so the tile is as large as
+// fits and the warps are few: 64 elements per thread and tile. (With 16, and a
+// third tile on chip to form the next sums ahead, more than half of the
+// instructions were overhead.)
 template <typename TX, typename TG, int E, int CPT, int W>
 struct NormGradTileCfg {
   static constexpr int KP = CPT * W * 32, THREADS = W * 32;
   static constexpr int SLOT_X = KP * int(sizeof(TX)) + StagedRow<TX, E>::PAD;
   static constexpr int SLOT = SLOT_X + KP * int(sizeof(TG)) + StagedRow<TG, E>::PAD;
-  // three tiles on chip, of as many rows as leave room for 4, 2 or 1 CTAs per SM
-  static constexpr int S = 3, LIMIT = (W <= 4 ? 50 : W <= 8 ? 100 : 200) * 1024;
-  static constexpr int R = S * 4 * SLOT <= LIMIT ? 4 : S * 2 * SLOT <= LIMIT ? 2 : 1;
+  static constexpr int CTAS = W <= 4 ? 3 : 1, LIMIT = 222 * 1024 / CTAS - KP * 4;
+  static constexpr int R = 2 * 8 * SLOT <= LIMIT ? 8 : 2 * 4 * SLOT <= LIMIT ? 4 : 2 * 2 * SLOT <= LIMIT ? 2 : 1;
   static constexpr int TILE = R * SLOT;
-  static constexpr int SMEM = S * TILE;
+  static constexpr int SMEM = 2 * TILE + KP * 4;
 };
 
 template <typename TX, typename TG, int E, int CPT, int W>
-__global__ void __launch_bounds__(W * 32)
+__global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::CTAS))
     layer_norm_grad_tile_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w,
                                 const float* __restrict__ mean, const float* __restrict__ rstd,
                                 const TG* __restrict__ dy, int64_t lddy, TX* __restrict__ dx, int64_t lddx,
@@ -429,143 +430,172 @@ __global__ void __launch_bounds__(W * 32)
   using C = NormGradTileCfg<TX, TG, E, CPT, W>;
   using RowX = StagedRow<TX, E>;
   using RowG = StagedRow<TG, E>;
-  constexpr int R = C::R, S = C::S;
-  static_assert(W % R == 0 && W <= 32 && S >= 3, "");
-  constexpr int P = W / R;  // warps to a row's sums
+  constexpr int R = C::R;
+  constexpr int P = W > R ? W / R : 1, Q = R > W ? R / W : 1;  // warps to a row's sums, rows to a warp
   constexpr int PAIRS = RowX::PAIRS, UNIT = E == 1 ? 2 : E, NU = CPT / UNIT, T = W * 32;
-  constexpr int NS = R * CPT / UNIT, TS = 32;  // the sums' units per lane
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float4 sums[2][W];     // of d, g and g d, by warp
-  __shared__ float2 kept[2][R];     // mean and rstd
+  constexpr int NS = C::KP / P / 32 / UNIT, TS = 32;  // the sums' units per lane and row
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ float4 sums[R * P];       // of d, g and g d
+  __shared__ float2 kept[R];           // mean and rstd
+  __shared__ float4 consts[R];         // -c, r, -md r, -r mean g
+  __shared__ float consts1[R];         // -r mean(g z)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int my_row = warp / P, my_part = warp % P;
+  const int my_row = P > 1 ? warp / P : warp * Q, my_part = P > 1 ? warp % P : 0;
   const int64_t tiles = (M + R - 1) / R;
-  uint8_t* ring = smem;
+  float* wplane = reinterpret_cast<float*>(smem);  // the weight, in planes of four columns
+  uint8_t* ring = smem + C::KP * 4;
 
-  auto fetch = [&](int slot, int64_t tile) {
-    if (tile < tiles) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int64_t m = tile * R + i;
-        if (m < M) {
-          uint8_t* at = ring + slot * C::TILE + i * C::SLOT;
-          RowX::template copy<C::KP, T>(at, x + m * ldx, K, m == 0, m == M - 1, tid);
-          RowG::template copy<C::KP, T>(at + C::SLOT_X, dy + m * lddy, K, m == 0, m == M - 1, tid);
-        }
-      }
-    }
-    cp_async_commit();
-  };
-  // what the forward pass kept of this warp's row of a tile
-  auto kept_of = [&](int64_t tile) {
-    const int64_t m = tile * R + my_row;
-    return tile < tiles && m < M ? make_float2(mean[m], rstd[m]) : make_float2(0.f, 0.f);
-  };
   const int64_t step = gridDim.x;
   int64_t tile = blockIdx.x;
 #pragma unroll
-  for (int i = 0; i < S * R; ++i) {
+  for (int i = 0; i < 2 * R; ++i) {
     RowX::template clear_pad<C::KP, T>(ring + i * C::SLOT, K, tid);
     RowG::template clear_pad<C::KP, T>(ring + i * C::SLOT + C::SLOT_X, K, tid);
   }
+  auto fetch = [&](int slot, int64_t t) {
+    const int rows = t >= tiles ? 0 : static_cast<int>(M - t * R < R ? M - t * R : R);
+    const TX* xt = x + t * R * ldx;
+    const TG* gt = dy + t * R * lddy;
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) fetch(i, tile + i * step);
+    for (int i = 0; i < R; ++i) {
+      if (i < rows) {
+        const bool first = t == 0 && i == 0, last = t == tiles - 1 && i == rows - 1;
+        uint8_t* at = ring + slot * C::TILE + i * C::SLOT;
+        RowX::template copy<C::KP, T>(at, xt, K, first, last, tid);
+        RowG::template copy<C::KP, T>(at + C::SLOT_X, gt, K, first, last, tid);
+      }
+      xt += ldx;
+      gt += lddy;
+    }
+    cp_async_commit();
+  };
+  // what the forward pass kept of this warp's rows of a tile
+  float2 k_cur[Q], k_next[Q];
+  auto kept_of = [&](int64_t t, float2(&k)[Q]) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int64_t m = t * R + my_row + q;
+      k[q] = m < M ? make_float2(mean[m], rstd[m]) : make_float2(0.f, 0.f);
+    }
+  };
+  fetch(0, tile);
+  kept_of(tile, k_next);
 
   // columns of the sums: a contiguous share of the row per warp
   auto sum_column = [&](int u) {
     return my_part * (C::KP / P) + (E == 1 ? lane + 64 * u : (lane + 32 * u) * E);
   };
   auto column = [&](int u) { return E == 1 ? tid + 2 * u * T : (tid + u * T) * E; };
-  auto weight_pair = [&](int k, int j, int stride) {
-    const int k0 = k + (E == 1 ? 0 : 2 * j), k1 = k0 + (E == 1 ? stride : 1);
-    return make_float2(w && k0 < K ? w[k0] : 1.f, w && k1 < K ? w[k1] : 1.f);
-  };
-  float2 ws[NS][PAIRS], wr[NU][PAIRS], aw[NU][PAIRS], ab[NU][PAIRS];
+  auto weights = [&](int k, int stride, float2(&f)[PAIRS]) {
+    if constexpr (E == 1) {
+      f[0] = make_float2(wplane[k], wplane[k + stride]);
+    } else {
 #pragma unroll
-  for (int u = 0; u < NS; ++u)
-#pragma unroll
-    for (int j = 0; j < PAIRS; ++j) ws[u][j] = weight_pair(sum_column(u), j, TS);
-#pragma unroll
-  for (int u = 0; u < NU; ++u)
-#pragma unroll
-    for (int j = 0; j < PAIRS; ++j) {
-      wr[u][j] = weight_pair(column(u), j, T);
-      aw[u][j] = ab[u][j] = both(0.f);
-    }
-  const float inv_k = 1.0f / static_cast<float>(K);
-
-  // sums of this warp's share of its row of the tile in `slot`
-  auto row_sums = [&](int64_t t, int slot, int buf, float2 k) {
-    const int64_t m = t * R + my_row;
-    if (t >= tiles || m >= M) return;
-    const uint8_t* at = ring + slot * C::TILE + my_row * C::SLOT;
-    const uint8_t *xs = RowX::first(at, x + m * ldx), *gs = RowG::first(at + C::SLOT_X, dy + m * lddy);
-    float2 s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
-#pragma unroll
-    for (int u = 0; u < NS; ++u) {
-      const int col = sum_column(u);
-      float2 fx[PAIRS], fg[PAIRS];
-      RowX::get(xs, col, TS, fx);
-      RowG::get(gs, col, TS, fg);
-      if constexpr (E == 1) {
-        fx[0] = make_float2(col < K ? fx[0].x : 0.f, col + TS < K ? fx[0].y : 0.f);
-        fg[0] = make_float2(col < K ? fg[0].x : 0.f, col + TS < K ? fg[0].y : 0.f);
+      for (int j = 0; j < PAIRS / 2; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(wplane + wb_at<E>(k + 4 * j, C::KP));
+        f[2 * j] = make_float2(v.x, v.y);
+        f[2 * j + 1] = make_float2(v.z, v.w);
       }
-      // behind the columns 0 - 0
-      const float2 cu = make_float2(col < K ? -k.x : 0.f, (E == 1 ? col + TS : col) < K ? -k.x : 0.f);
-      float2 gd[PAIRS];
-#pragma unroll
-      for (int j = 0; j < PAIRS; ++j) {
-        fx[j] = add2(fx[j], cu);
-        fg[j] = mul2(fg[j], ws[u][j]);
-        gd[j] = mul2(fg[j], fx[j]);
-      }
-      s0 = add2(s0, tree_sum2<PAIRS>(fx));
-      s1 = add2(s1, tree_sum2<PAIRS>(fg));
-      s2 = add2(s2, tree_sum2<PAIRS>(gd));
-    }
-    const float t0 = warp_sum(s0.x + s0.y), t1 = warp_sum(s1.x + s1.y), t2 = warp_sum(s2.x + s2.y);
-    if (lane == 0) {
-      sums[buf][warp] = make_float4(t0, t1, t2, 0.f);
-      if (my_part == 0) kept[buf][my_row] = k;
     }
   };
-
-  float2 k_next = kept_of(tile);
-  cp_async_wait<S - 2>();
+  for (int k = tid; k < C::KP; k += T) wplane[wb_at<E>(k, C::KP)] = w && k < K ? w[k] : 1.f;
   __syncthreads();
-  row_sums(tile, 0, 0, k_next);
-  k_next = kept_of(tile + step);
-  int slot = 0, buf = 0;
-  for (; tile < tiles; tile += step) {
-    cp_async_wait<S - 3>();
-    __syncthreads();  // the next tile has arrived, this one's sums are there, the last one's slot is free
-    const int next = slot + 1 == S ? 0 : slot + 1;
-    fetch(slot == 0 ? S - 1 : slot - 1, tile + (S - 1) * step);
-    const float2 k_cur = k_next;
-    k_next = kept_of(tile + 2 * step);
-    row_sums(tile + step, next, buf ^ 1, k_cur);
-
-    // lane l: the sums of warp l; after the exchange, of row l / P
-    float4 v = sums[buf][lane % W];
+  float2 wr[NU][PAIRS], aw[NU][PAIRS], ab[NU][PAIRS];
 #pragma unroll
-    for (int o = 1; o < P; o <<= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-      v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+  for (int u = 0; u < NU; ++u) {
+    weights(column(u), T, wr[u]);
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) aw[u][j] = ab[u][j] = both(0.f);
+  }
+  const float inv_k = 1.0f / static_cast<float>(K);
+  // a row's constants from its sums
+  auto finish = [&](int row, float4 v, float2 k) {
+    const float md = v.x * inv_k, mg = v.y * inv_k, mgz = k.y * (v.z - md * v.y) * inv_k;
+    consts[row] = make_float4(-k.x, k.y, -md * k.y, -k.y * mg);
+    consts1[row] = -k.y * mgz;
+  };
+
+  int slot = 0;
+  for (; tile < tiles; tile += step) {
+    const int rows = static_cast<int>(M - tile * R < R ? M - tile * R : R);
+    const TX* xt = x + tile * R * ldx;
+    const TG* gt = dy + tile * R * lddy;
+    cp_async_wait<0>();
+    __syncthreads();  // the tile has arrived; the other slot and the constants are free
+    fetch(slot ^ 1, tile + step);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) k_cur[q] = k_next[q];
+    kept_of(tile + step, k_next);
+
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int row = my_row + q;
+      if (row < rows) {
+        const uint8_t* at = ring + slot * C::TILE + row * C::SLOT;
+        const uint8_t *xs = RowX::first(at, xt + row * ldx), *gs = RowG::first(at + C::SLOT_X, gt + row * lddy);
+        float2 s0[2], s1[2], s2[2];
+        s0[0] = s0[1] = s1[0] = s1[1] = s2[0] = s2[1] = both(0.f);
+        const float c = k_cur[q].x;
+#pragma unroll 8
+        for (int u = 0; u < NS; ++u) {
+          const int col = sum_column(u);
+          float2 fx[PAIRS], fg[PAIRS], ws[PAIRS];
+          RowX::get(xs, col, TS, fx);
+          RowG::get(gs, col, TS, fg);
+          weights(col, TS, ws);
+          if constexpr (E == 1) {
+            fx[0] = make_float2(col < K ? fx[0].x : 0.f, col + TS < K ? fx[0].y : 0.f);
+            fg[0] = make_float2(col < K ? fg[0].x : 0.f, col + TS < K ? fg[0].y : 0.f);
+          }
+          // behind the columns 0 - 0
+          const float2 cu = make_float2(col < K ? -c : 0.f, (E == 1 ? col + TS : col) < K ? -c : 0.f);
+#pragma unroll
+          for (int j = 0; j < PAIRS; ++j) {
+            const int h = PAIRS > 1 ? j & 1 : u & 1;
+            fx[j] = add2(fx[j], cu);
+            fg[j] = mul2(fg[j], ws[j]);
+            s0[h] = add2(s0[h], fx[j]);
+            s1[h] = add2(s1[h], fg[j]);
+            s2[h] = fma2(fg[j], fx[j], s2[h]);
+          }
+        }
+        s0[0] = add2(s0[0], s0[1]);
+        s1[0] = add2(s1[0], s1[1]);
+        s2[0] = add2(s2[0], s2[1]);
+        float4 v = make_float4(warp_sum(s0[0].x + s0[0].y), warp_sum(s1[0].x + s1[0].y), warp_sum(s2[0].x + s2[0].y), 0.f);
+        if (lane == 0) {
+          if constexpr (P == 1) {
+            finish(row, v, k_cur[q]);
+          } else {
+            sums[warp] = v;
+            if (my_part == 0) kept[row] = k_cur[q];
+          }
+        }
+      }
     }
-    const float2 kr = kept[buf][(lane % W) / P];
-    const float md = v.x * inv_k, mg = v.y * inv_k, mgz = kr.y * (v.z - md * v.y) * inv_k;
-    const float l_zs = -md * kr.y, l_o0 = -kr.y * mg, l_o1 = -kr.y * mgz;
+    __syncthreads();  // the sums
+    if constexpr (P > 1) {
+      if (tid < R) {
+        float4 v = sums[tid * P];
+#pragma unroll
+        for (int i = 1; i < P; ++i) {
+          const float4 a = sums[tid * P + i];
+          v.x += a.x;
+          v.y += a.y;
+          v.z += a.z;
+        }
+        finish(tid, v, kept[tid]);
+      }
+      __syncthreads();
+    }
+    TX* dxt = dx + (dx ? tile * R * lddx : 0);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int64_t m = tile * R + i;
-      const float c = __shfl_sync(0xffffffffu, kr.x, i * P), r = __shfl_sync(0xffffffffu, kr.y, i * P);
-      const float2 zs = both(__shfl_sync(0xffffffffu, l_zs, i * P));
-      const float2 o0 = both(__shfl_sync(0xffffffffu, l_o0, i * P)), o1 = both(__shfl_sync(0xffffffffu, l_o1, i * P));
-      if (m >= M) break;
+      if (i >= rows) break;
+      const float4 q = consts[i];
+      const float2 c = both(q.x), r = both(q.y), zs = both(q.z), o0 = both(q.w), o1 = both(consts1[i]);
       const uint8_t* at = ring + slot * C::TILE + i * C::SLOT;
-      const uint8_t *xs = RowX::first(at, x + m * ldx), *gs = RowG::first(at + C::SLOT_X, dy + m * lddy);
+      const uint8_t *xs = RowX::first(at, xt + i * ldx), *gs = RowG::first(at + C::SLOT_X, gt + i * lddy);
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         const int k = column(u);
@@ -574,29 +604,34 @@ __global__ void __launch_bounds__(W * 32)
         RowG::get(gs, k, T, fg);
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
-          const float2 z = fma2(add2(fx[j], both(-c)), both(r), zs);
+          const float2 z = fma2(add2(fx[j], c), r, zs);
           aw[u][j] = fma2(fg[j], z, aw[u][j]);
           ab[u][j] = add2(ab[u][j], fg[j]);
-          fx[j] = fma2(mul2(fg[j], wr[u][j]), both(r), fma2(z, o1, o0));
+          fx[j] = fma2(mul2(fg[j], wr[u][j]), r, fma2(z, o1, o0));
         }
-        if (dx && k < K) put_unit<TX, E>(dx + m * lddx, k, T, K, fx);
+        if (dx && k < K) put_unit<TX, E>(dxt + i * lddx, k, T, K, fx);
       }
     }
-    slot = next;
-    buf ^= 1;
+    slot ^= 1;
   }
   if (!part) return;
   grid_dependents_launch();
   float* pw = part + static_cast<int64_t>(blockIdx.x) * K;
   float* pb = pw + static_cast<int64_t>(gridDim.x) * K;
 #pragma unroll
-  for (int u = 0; u < NU; ++u)
+  for (int u = 0; u < NU; ++u) {
+    const int k = column(u);
+    if constexpr (E == 1) {
+      if (k < K) pw[k] = aw[u][0].x, pb[k] = ab[u][0].x;
+      if (k + T < K) pw[k + T] = aw[u][0].y, pb[k + T] = ab[u][0].y;
+    } else if (k < K) {  // K is a multiple of four here
 #pragma unroll
-    for (int j = 0; j < PAIRS; ++j) {
-      const int k0 = column(u) + (E == 1 ? 0 : 2 * j), k1 = k0 + (E == 1 ? T : 1);
-      if (k0 < K) pw[k0] = aw[u][j].x, pb[k0] = ab[u][j].x;
-      if (k1 < K) pw[k1] = aw[u][j].y, pb[k1] = ab[u][j].y;
+      for (int j = 0; j < PAIRS; j += 2) {
+        *reinterpret_cast<float4*>(pw + k + 2 * j) = make_float4(aw[u][j].x, aw[u][j].y, aw[u][j + 1].x, aw[u][j + 1].y);
+        *reinterpret_cast<float4*>(pb + k + 2 * j) = make_float4(ab[u][j].x, ab[u][j].y, ab[u][j + 1].x, ab[u][j + 1].y);
+      }
     }
+  }
 }
 
 // Rows too long for that: dx and the weight's gradient separately, from two
