@@ -566,13 +566,15 @@ NormWs norm_ws(int64_t M, int64_t K) {
 }
 
 struct EmbedWs {
-  int64_t chunks;
-  size_t key[2], val[2], touched, num_heavy, heavy, part, bytes;
+  int64_t chunk, chunks;  // sorted positions per warp of the sums
+  size_t key[2], val[2], num_heavy, heavy, part, bytes;
 };
 EmbedWs embed_ws(int64_t T, int64_t V, int64_t D) {
   EmbedWs w{};
   if (T < 1 || V < 1 || D < 1 || T > kMaxIds || V > kMaxIds || D > kMaxDim || T >= kMaxProduct / D) return w;
-  w.chunks = cdiv(T, kEgChunk);
+  // chunks of 32 unless their warps (of 256 columns) would be fewer than 32 per SM
+  w.chunk = cdiv(T, kEgChunk) * cdiv(D, kEgCols) < 148 * 32 ? kEgShort : kEgChunk;
+  w.chunks = cdiv(T, w.chunk);
   size_t at = 0;
   auto take = [&at](size_t bytes) {
     const size_t a = at;
@@ -583,11 +585,10 @@ EmbedWs embed_ws(int64_t T, int64_t V, int64_t D) {
     w.key[i] = take(size_t(T) * 4);
     w.val[i] = take(size_t(T) * 4);
   }
-  w.touched = take(size_t(cdiv(V, 32)) * 4);
   w.num_heavy = take(4);
   w.heavy = take(size_t(w.chunks) * sizeof(EmbedHeavy));
   w.part = take(size_t(2 * w.chunks) * size_t(D) * 4);
-  w.bytes = at;
+  w.bytes = at + 256;  // the sections begin at the first 256-byte boundary
   return w;
 }
 
@@ -662,7 +663,7 @@ inline int64_t persistent_grid(int ctas_per_sm, int sms, int64_t units, int64_t 
 // launch with programmatic serialisation: the kernel may be scheduled while
 // the one before it runs, and waits for it by itself
 template <typename... Params, typename... Args>
-int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -1266,8 +1267,12 @@ int bl_embedding(const void* ids, int id_type, const void* table, int table_type
     using TY = decltype(ty);
     auto run = [&](auto ti, auto e) {
       using TI = decltype(ti);
-      embedding_kernel<TI, TT, TY, decltype(e)::value><<<static_cast<unsigned>(T), kEmbThreads, 0, s>>>(
-          static_cast<const TI*>(ids), static_cast<const TT*>(table), static_cast<TY*>(y), T, V, D, scale);
+      constexpr int E = decltype(e)::value;
+      const int64_t tiles = cdiv(D, kEmbBatch * 32 * E);
+      if (T * tiles > int64_t(0xFFFFFFFF)) return int(BL_ERR_UNSUPPORTED);
+      embedding_kernel<TI, TT, TY, E><<<static_cast<unsigned>(cdiv(T * tiles, kEmbThreads / 32)), kEmbThreads, 0, s>>>(
+          static_cast<const TI*>(ids), static_cast<const TT*>(table), static_cast<TY*>(y), uint32_t(T), V, D,
+          uint32_t(tiles), scale);
       return launch_status();
     };
     using E1 = Int<1>;
@@ -1302,13 +1307,12 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
   int sms = 0;
   int rc = device_setup(&sms);
   if (rc != BL_OK) return rc;
-  uint8_t* base = static_cast<uint8_t*>(ws);
+  uint8_t* base = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(ws)));
   EmbedSort p;
   for (int i = 0; i < 2; ++i) {
     p.key[i] = reinterpret_cast<uint32_t*>(base + w.key[i]);
     p.val[i] = reinterpret_cast<uint32_t*>(base + w.val[i]);
   }
-  p.touched = reinterpret_cast<uint32_t*>(base + w.touched);
   p.num_heavy = reinterpret_cast<uint32_t*>(base + w.num_heavy);
   p.heavy = reinterpret_cast<EmbedHeavy*>(base + w.heavy);
   float* part = reinterpret_cast<float*>(base + w.part);
@@ -1317,33 +1321,46 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
   while ((V >> bits) != 0) ++bits;
   const int passes = (bits + 7) / 8, digit_bits = (bits + passes - 1) / passes;
   const uint32_t t32 = static_cast<uint32_t>(T), v32 = static_cast<uint32_t>(V);
-  if (id_type == BL_IDS_I64)
-    embed_sort_kernel<int64_t><<<kEsCluster, kEsThreads, 0, s>>>(static_cast<const int64_t*>(ids), t32, v32, padding_id,
-                                                                 passes, digit_bits, p);
-  else
-    embed_sort_kernel<int32_t><<<kEsCluster, kEsThreads, 0, s>>>(static_cast<const int32_t*>(ids), t32, v32, padding_id,
-                                                                 passes, digit_bits, p);
-  if ((rc = launch_status()) != BL_OK) return rc;
   const uint32_t* key = p.key[(passes + 1) & 1];
   const uint32_t* val = p.val[(passes + 1) & 1];
-  const int64_t sum_blocks = cdiv(w.chunks * cdiv(D, kEgCols), kEgWarps);
-  const int64_t zero_blocks = acc ? 0 : std::min<int64_t>(cdiv(V, kEgWarps), int64_t(sms) * 8);
+  // writers of zeros: a CTA on each SM that does not sort, and rows for each of its warps
+  const unsigned zero_grid = static_cast<unsigned>(std::min<int64_t>(cdiv(V, kEsWarps), std::max(1, sms - kEsCluster)));
+  const unsigned sum_grid = static_cast<unsigned>(cdiv(w.chunks * cdiv(D, kEgCols), kEgWarps));
+  const uint32_t chunk = static_cast<uint32_t>(w.chunk);
   const bool vec = rows_vec(dy, dy_type, D, D, 1) && rows_vec(dtable, table_type, D, D, 1);
+  auto sort = [&](auto ti) {
+    using TI = decltype(ti);
+    embed_sort_kernel<TI><<<kEsCluster, kEsThreads, 0, s>>>(static_cast<const TI*>(ids), t32, v32, padding_id, passes,
+                                                            digit_bits, chunk, p);
+    return launch_status();
+  };
+  rc = id_type == BL_IDS_I64 ? sort(int64_t{}) : sort(int32_t{});
+  if (rc != BL_OK) return rc;
   return with_types(dy_type, table_type, [&](auto tg, auto tt) {
     using TG = decltype(tg);
     using TT = decltype(tt);
+    auto* out = static_cast<TT*>(dtable);
     auto run = [&](auto e, auto a) {
       constexpr int E = decltype(e)::value;
       constexpr bool ACC = decltype(a)::value;
-      embed_grad_kernel<TG, TT, E, ACC><<<static_cast<unsigned>(sum_blocks + zero_blocks), kEgWarps * 32, 0, s>>>(
-          key, val, p.touched, static_cast<const TG*>(dy), static_cast<TT*>(dtable), part, t32, v32, D, scale,
-          static_cast<uint32_t>(sum_blocks));
-      int st = launch_status();
+      int st = BL_OK;
+      if (!ACC)
+        st = id_type == BL_IDS_I64
+                 ? launch_after(embed_zero_kernel<int64_t, TT, E>, dim3(zero_grid), kEsThreads, 0, s,
+                                static_cast<const int64_t*>(ids), t32, v32, padding_id, out, D)
+                 : launch_after(embed_zero_kernel<int32_t, TT, E>, dim3(zero_grid), kEsThreads, 0, s,
+                                static_cast<const int32_t*>(ids), t32, v32, padding_id, out, D);
+      if (st != BL_OK) return st;
+      constexpr auto by_32 = embed_grad_kernel<TG, TT, E, kEgChunk, ACC>;
+      constexpr auto by_8 = embed_grad_kernel<TG, TT, E, kEgShort, ACC>;
+      st = launch_after(w.chunk == kEgChunk ? by_32 : by_8, dim3(sum_grid), kEgWarps * 32, 0, s, key, val,
+                        static_cast<const TG*>(dy), out, part, t32, v32, D, scale);
       if (st != BL_OK || w.chunks < 3) return st;  // a long segment spans three chunks
-      const int64_t most = (w.chunks / 2) * cdiv(D, 32);
-      embed_grad_heavy_kernel<TT, ACC><<<static_cast<unsigned>(std::min<int64_t>(most, int64_t(sms) * 8)), kEgWarps * 32,
-                                         0, s>>>(key, p.num_heavy, p.heavy, part, static_cast<TT*>(dtable), D, scale);
-      return launch_status();
+      constexpr int HE = E == 8 ? 8 : 1;
+      const int64_t most = cdiv((w.chunks / 2) * cdiv(D, 32 * HE), kEgWarps);
+      return launch_after(embed_grad_heavy_kernel<TT, HE, ACC>, dim3(unsigned(std::min<int64_t>(most, int64_t(sms) * 4))),
+                          kEgWarps * 32, 0, s, key, static_cast<const uint32_t*>(p.num_heavy),
+                          static_cast<const EmbedHeavy*>(p.heavy), static_cast<const float*>(part), out, chunk, D, scale);
     };
     using E1 = Int<1>;
     using E8 = Int<8>;
@@ -1391,43 +1408,57 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
     if (rc != BL_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     double* sums = static_cast<double*>(ws);
-    const int ctas = std::min(sms * 4, kGcMaxCtas);
-    static thread_local GcParams<kGcMaxTensors> P;
+    const int ctas = std::min(sms * 8, kGcMaxCtas);
     // launches of up to kGcMaxTensors tensors: all the norms, then all the products
     int num_sums = 0;
-    for (int pass = 0; pass < 2; ++pass) {
+    auto pass = [&](auto cap, bool norms) {
+      constexpr int CAP = decltype(cap)::value;
+      static thread_local GcParams<CAP> P;
       int i = 0, launch = 0;
       do {
-        P.n = 0;
+        int n = 0;
         int64_t chunks = 0;
         bool writes = false;
-        for (; i < num_tensors && P.n < kGcMaxTensors; ++i) {
+        for (; i < num_tensors && n < CAP; ++i) {
           const bl_grad_tensor& t = tensors[i];
           if (t.numel == 0) continue;
           const int es = type_bytes(t.type);
-          P.t[P.n] = GcTensor{t.g, t.out, t.numel};
-          P.f32[P.n] = t.type == BL_TYPE_F32;
-          P.chunk0[P.n] = static_cast<int32_t>(chunks);
+          P.t[n] = GcTensor{t.g, t.out, t.numel};
+          P.f32[n] = t.type == BL_TYPE_F32;
+          P.chunk0[n] = static_cast<int32_t>(chunks);
           const int64_t mis = int64_t(reinterpret_cast<uintptr_t>(t.g) & 15u) / es;
           chunks += cdiv(t.numel + mis, int64_t(kGcChunkVecs) * 16 / es);
           writes |= t.out != nullptr;
-          ++P.n;
+          ++n;
         }
-        P.chunk0[P.n] = static_cast<int32_t>(chunks);
+        P.chunk0[n] = static_cast<int32_t>(chunks);
         const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, ctas)));
-        if (pass == 0) {
-          grad_norm_kernel<kGcMaxTensors><<<grid, kGcThreads, 0, s>>>(P, sums + num_sums);
+        for (int b = 0, at = 0; b <= grid; ++b) {
+          const int c = std::min(gc_begin(int(chunks), b, grid), std::max(0, int(chunks) - 1));
+          while (at + 1 < n && P.chunk0[at + 1] <= c) ++at;
+          P.first[b] = static_cast<uint16_t>(at);
+        }
+        int st = BL_OK;
+        if (norms) {
+          grad_norm_kernel<CAP><<<grid, kGcThreads, 0, s>>>(P, int(chunks), sums + num_sums);
           num_sums += grid;
+          st = launch_status();
         } else if (writes || launch == 0) {
-          grad_scale_kernel<kGcMaxTensors><<<writes ? grid : 1, kGcThreads, 0, s>>>(P, sums, num_sums, max_norm,
-                                                                                    launch == 0 ? stats : nullptr);
+          st = launch_after(grad_scale_kernel<CAP>, dim3(writes ? unsigned(grid) : 1u), kGcThreads, 0, s, P, writes ? int(chunks) : 0,
+                            static_cast<const double*>(sums), num_sums, max_norm, launch == 0 ? stats : nullptr);
         }
         ++launch;
-        const int st = launch_status();
         if (st != BL_OK) return st;
       } while (i < num_tensors);
-    }
-    return BL_OK;
+      return int(BL_OK);
+    };
+    // descriptors are copied with each launch: no more of them than there are
+    auto run = [&](auto cap) {
+      const int st = pass(cap, true);
+      return st != BL_OK ? st : pass(cap, false);
+    };
+    if (num_tensors <= 32) return run(Int<32>{});
+    return num_tensors <= 256 ? run(Int<256>{}) : run(Int<kGcMaxTensors>{});
   } catch (...) {  // out of host memory
     return BL_ERR_CUDA;
   }

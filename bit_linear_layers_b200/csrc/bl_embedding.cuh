@@ -6,13 +6,14 @@
 // would make the order, and so the rounding, of frequent tokens' sums differ
 // from run to run; here the tokens are first sorted by id (stable: the rows of
 // a token are added in the order of their positions), then the sorted list is
-// cut into chunks of 32 positions and one warp per (chunk, 256 columns) adds
-// up the segments that start in its chunk. A segment that ends in the next
-// chunk is finished by the warp that began it (at most 63 rows); a longer one
-// is summed chunk by chunk into fp32 partial rows that a last kernel adds up
-// in order, so a token that fills the batch is as parallel as any other. Rows
-// of the table that no token names are zero-filled by the same launch as the
-// sums: each element of dE is written once.
+// cut into chunks of 32 positions (8 in a short list) and one warp per (chunk,
+// 256 columns) adds up the segments that start in its chunk. A segment that ends
+// in the next chunk is finished by the warp that began it; a longer one is
+// summed chunk by chunk into fp32 partial rows that a last kernel adds up in
+// order, so a token that fills the batch is as parallel as any other.
+// Most of the table's rows have no token, and zero-filling them is most of the
+// traffic: a second kernel writes zeros to the rows that no token names while
+// one cluster of eight SMs sorts, and each element of dE is written once.
 #pragma once
 
 #include "bl_elem.cuh"
@@ -27,26 +28,38 @@ __device__ __forceinline__ int64_t embed_row(const TI* ids, int64_t t, int64_t V
 }
 
 constexpr int kEmbThreads = 256;
+constexpr int kEmbBatch = 4;  // accesses in flight per lane
 
-// One CTA per token (grid-stride); a token outside the table gets a row of zeros.
+// One warp per token and kEmbBatch * 32 accesses of its row; a token outside
+// the table gets a row of zeros.
 template <typename TI, typename TT, typename TY, int E>
 __global__ void __launch_bounds__(kEmbThreads)
-    embedding_kernel(const TI* __restrict__ ids, const TT* __restrict__ table, TY* __restrict__ y, int64_t T,
-                     int64_t V, int64_t D, float scale) {
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int64_t row = embed_row(ids, t, V);
-    if (row < 0 && threadIdx.x == 0) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingId);
-    for (int64_t k = static_cast<int64_t>(threadIdx.x) * E; k < D; k += kEmbThreads * E) {
-      float f[E];
-      if (row >= 0) {
-        Elem<TT, E>::load(table + row * D + k, f);
+    embedding_kernel(const TI* __restrict__ ids, const TT* __restrict__ table, TY* __restrict__ y, uint32_t T,
+                     int64_t V, int64_t D, uint32_t tiles, float scale) {
+  const uint32_t item = blockIdx.x * (kEmbThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const uint32_t t = item / tiles, tile = item % tiles;
+  if (t >= T) return;
+  const int64_t row = embed_row(ids, t, V);
+  if (row < 0 && lane == 0 && tile == 0) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingId);
+  const int64_t k0 = static_cast<int64_t>(tile) * (kEmbBatch * 32 * E) + lane * E;
+  float f[kEmbBatch][E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] *= scale;
-      } else {
+  for (int u = 0; u < kEmbBatch; ++u) {
+    const int64_t k = k0 + u * (32 * E);
+    if (k < D && row >= 0) {
+      Elem<TT, E>::load(table + row * D + k, f[u]);
+    } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] = 0.f;
-      }
-      Elem<TY, E>::store(y + t * D + k, f);
+      for (int j = 0; j < E; ++j) f[u][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kEmbBatch; ++u) {
+    const int64_t k = k0 + u * (32 * E);
+    if (k < D) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) f[u][j] *= scale;
+      Elem<TY, E>::store(y + static_cast<int64_t>(t) * D + k, f[u]);
     }
   }
 }
@@ -62,7 +75,8 @@ constexpr int kEsCluster = 8;
 constexpr int kEsThreads = 1024;
 constexpr int kEsWarps = kEsThreads / 32;
 constexpr int kEsBins = 256;
-constexpr int kEgChunk = 32;  // sorted positions per warp of the sums
+constexpr int kEsHold = 8;    // positions per lane that are held between counting and placing
+constexpr int kEzRows = 8192 * 32;  // rows of the table whose bits fit the shared memory of a CTA
 
 struct EmbedHeavy {
   uint32_t first, last;  // the chunks in which a long segment starts and ends
@@ -71,7 +85,6 @@ struct EmbedHeavy {
 struct EmbedSort {
   uint32_t* key[2];
   uint32_t* val[2];
-  uint32_t* touched;    // bit v: some token names row v
   uint32_t* num_heavy;
   EmbedHeavy* heavy;
 };
@@ -91,11 +104,17 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t smem_addr, uint32_t 
 }
 
 template <typename TI>
-__global__ void __cluster_dims__(kEsCluster, 1, 1) __launch_bounds__(kEsThreads)
-    embed_sort_kernel(const TI* __restrict__ ids, uint32_t T, uint32_t V, int64_t padding_id, int passes, int digit_bits,
-                      EmbedSort p) {
-  __shared__ uint32_t hist[kEsWarps][kEsBins];  // counts, then next output positions
-  __shared__ uint32_t tot[kEsBins];             // this CTA's counts, read by the cluster
+__device__ __forceinline__ uint32_t embed_key(const TI* ids, uint32_t i, uint32_t V, int64_t padding_id) {
+  const int64_t id = static_cast<int64_t>(ids[i]);
+  return id >= 0 && id < V && id != padding_id ? static_cast<uint32_t>(id) : V;
+}
+
+template <typename TI>
+__device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* __restrict__ ids, uint32_t T, uint32_t V,
+                                           int64_t padding_id, int passes, int digit_bits, uint32_t chunk,
+                                           const EmbedSort& p) {
+  __shared__ uint32_t tot[kEsBins];         // this CTA's counts, read by the cluster
+  __shared__ uint32_t quarter[4][kEsBins];  // of eight warps each
   __shared__ uint32_t wsum[kEsBins / 32];
   const uint32_t rank = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t gtid = rank * kEsThreads + tid;
@@ -103,7 +122,7 @@ __global__ void __cluster_dims__(kEsCluster, 1, 1) __launch_bounds__(kEsThreads)
   // whole warps of positions: a warp's run, then a CTA's
   const uint32_t run = ((T + kAll - 1) / kAll) * 32;
   const uint32_t w0 = min(T, (rank * kEsWarps + warp) * run), w1 = min(T, w0 + run);
-  for (uint32_t i = gtid; i < (V + 31) / 32; i += kAll) p.touched[i] = 0u;
+  const bool hold = run <= kEsHold * 32;
   if (gtid == 0) *p.num_heavy = 0u;
   const uint32_t mask = (1u << digit_bits) - 1u;
 
@@ -113,73 +132,96 @@ __global__ void __cluster_dims__(kEsCluster, 1, 1) __launch_bounds__(kEsThreads)
     const uint32_t* vin = p.val[(pass + 1) & 1];
     uint32_t* kout = p.key[pass & 1];
     uint32_t* vout = p.val[pass & 1];
-    auto key_at = [&](uint32_t i) -> uint32_t {
-      if (pass > 0) return __ldcg(kin + i);
-      const int64_t id = static_cast<int64_t>(ids[i]);
-      return id >= 0 && id < V && id != padding_id ? static_cast<uint32_t>(id) : V;
+    uint32_t kh[kEsHold], vh[kEsHold];
+    // the block of positions b0 + 32 u + lane (key V + 1: none)
+    auto load = [&](uint32_t b0) {
+#pragma unroll
+      for (int u = 0; u < kEsHold; ++u) {
+        const uint32_t i = b0 + 32 * u + lane;
+        kh[u] = V + 1;
+        if (i < w1) {
+          kh[u] = pass > 0 ? __ldcg(kin + i) : embed_key(ids, i, V, padding_id);
+          vh[u] = pass > 0 ? __ldcg(vin + i) : i;
+        }
+      }
     };
     for (int d = lane; d < kEsBins; d += 32) hist[warp][d] = 0u;
     __syncwarp();
-    for (uint32_t i = w0 + lane; i < w1; i += 32) atomicAdd(&hist[warp][(key_at(i) >> shift) & mask], 1u);
+    for (uint32_t b0 = w0; b0 < w1; b0 += kEsHold * 32) {
+      load(b0);
+#pragma unroll
+      for (int u = 0; u < kEsHold; ++u)
+        if (kh[u] <= V) atomicAdd(&hist[warp][(kh[u] >> shift) & mask], 1u);
+    }
     __syncthreads();
     // digit d: counts of the warps ahead, this CTA's total
-    if (tid < kEsBins) {
-      uint32_t t = 0;
-      for (int w = 0; w < kEsWarps; ++w) {
-        const uint32_t c = hist[w][tid];
-        hist[w][tid] = t;
-        t += c;
-      }
-      tot[tid] = t;
-    }
-    cluster_barrier();
-    uint32_t below = 0, all = 0;
-    if (tid < kEsBins) {
-      for (uint32_t r = 0; r < kEsCluster; ++r) {
-        const uint32_t c = ld_cluster_u32(smem_u32(&tot[tid]), r);
-        below += r < rank ? c : 0u;
-        all += c;
-      }
-      // exclusive sum of `all` over the digits
-      uint32_t inc = all;
+    const uint32_t d = tid & (kEsBins - 1), q = tid / kEsBins;
+    uint32_t c[kEsWarps / 4], sum = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= static_cast<uint32_t>(o)) inc += u;
-      }
-      if (lane == 31) wsum[warp] = inc;
-      below += inc - all;
+    for (int w = 0; w < kEsWarps / 4; ++w) c[w] = hist[q * (kEsWarps / 4) + w][d];
+#pragma unroll
+    for (int w = 0; w < kEsWarps / 4; ++w) {
+      const uint32_t x = c[w];
+      c[w] = sum;
+      sum += x;
     }
+    quarter[q][d] = sum;
     __syncthreads();
-    if (tid < kEsBins) {
-      for (uint32_t w = 0; w < warp; ++w) below += wsum[w];
-      for (int w = 0; w < kEsWarps; ++w) hist[w][tid] += below;
+    uint32_t ahead = 0, all4 = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t x = quarter[i][d];
+      ahead += i < q ? x : 0u;
+      all4 += x;
     }
+    if (q == 0) tot[d] = all4;
+    cluster_barrier();
+    uint32_t below = 0, all = 0, inc = 0;
+    uint32_t x[kEsCluster];
+#pragma unroll
+    for (uint32_t r = 0; r < kEsCluster; ++r) x[r] = ld_cluster_u32(smem_u32(&tot[d]), r);
+#pragma unroll
+    for (uint32_t r = 0; r < kEsCluster; ++r) {
+      below += r < rank ? x[r] : 0u;
+      all += x[r];
+    }
+    // exclusive sum of `all` over the digits (the four quarters of the threads do the same)
+    inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= static_cast<uint32_t>(o)) inc += u;
+    }
+    if (q == 0 && lane == 31) wsum[d / 32] = inc;
     __syncthreads();
-    for (uint32_t i0 = w0; i0 < w1; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      const bool live = i < w1;
-      uint32_t key = 0, val = 0, d = kEsBins;
-      if (live) {
-        key = key_at(i);
-        val = pass > 0 ? __ldcg(vin + i) : i;
-        d = (key >> shift) & mask;
-        if (pass == 0 && key < V) atomicOr(&p.touched[key >> 5], 1u << (key & 31));
-        if (pass == 0 && key == V) {
-          const int64_t id = static_cast<int64_t>(ids[i]);
+    uint32_t base = below + inc - all + ahead;
+#pragma unroll
+    for (uint32_t w = 0; w < kEsBins / 32; ++w) base += w < d / 32 ? wsum[w] : 0u;
+#pragma unroll
+    for (int w = 0; w < kEsWarps / 4; ++w) hist[q * (kEsWarps / 4) + w][d] = c[w] + base;
+    __syncthreads();
+    for (uint32_t b0 = w0; b0 < w1; b0 += kEsHold * 32) {
+      if (!hold) load(b0);
+#pragma unroll
+      for (int u = 0; u < kEsHold; ++u) {
+        if (b0 + 32 * u >= w1) break;  // uniform over the warp
+        const bool live = kh[u] <= V;
+        const uint32_t dig = live ? (kh[u] >> shift) & mask : kEsBins;
+        if (pass == 0 && kh[u] == V) {
+          const int64_t id = static_cast<int64_t>(ids[vh[u]]);
           if (id < 0 || id >= V) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingGradId);
         }
-      }
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      const uint32_t before = __popc(same & ((1u << lane) - 1u));
-      uint32_t at = 0;
-      if (live) at = hist[warp][d] + before;
-      __syncwarp();
-      if (live && before == 0) hist[warp][d] += __popc(same);
-      __syncwarp();
-      if (live) {
-        kout[at] = key;
-        vout[at] = val;
+        const uint32_t same = __match_any_sync(0xffffffffu, dig);
+        const uint32_t before = __popc(same & ((1u << lane) - 1u));
+        uint32_t at = 0;
+        if (live) at = hist[warp][dig] + before;
+        __syncwarp();
+        if (live && before == 0) hist[warp][dig] += __popc(same);
+        __syncwarp();
+        if (live) {
+          kout[at] = kh[u];
+          vout[at] = vh[u];
+        }
       }
     }
     cluster_barrier();  // the sorted list, and `tot` read by everyone
@@ -187,15 +229,15 @@ __global__ void __cluster_dims__(kEsCluster, 1, 1) __launch_bounds__(kEsThreads)
 
   // list the segments that reach past the chunk after the one they start in
   const uint32_t* key = p.key[(passes + 1) & 1];
-  const uint32_t chunks = (T + kEgChunk - 1) / kEgChunk;
+  const uint32_t chunks = (T + chunk - 1) / chunk;
   for (uint32_t c = gtid; c + 2 < chunks; c += kAll) {
-    const uint32_t h = __ldcg(key + (c + 1) * kEgChunk - 1);
-    if (h == V || __ldcg(key + (c + 2) * kEgChunk) != h) continue;
-    if (c > 0 && __ldcg(key + c * kEgChunk - 1) == h) continue;  // it started earlier
+    const uint32_t h = __ldcg(key + (c + 1) * chunk - 1);
+    if (h == V || __ldcg(key + (c + 2) * chunk) != h) continue;
+    if (c > 0 && __ldcg(key + c * chunk - 1) == h) continue;  // it started earlier
     uint32_t lo = c + 2, hi = chunks;  // chunk lo starts with h, chunk hi does not
     while (hi - lo > 1) {
       const uint32_t mid = lo + (hi - lo) / 2;
-      if (__ldcg(key + mid * kEgChunk) == h)
+      if (__ldcg(key + mid * chunk) == h)
         lo = mid;
       else
         hi = mid;
@@ -204,69 +246,141 @@ __global__ void __cluster_dims__(kEsCluster, 1, 1) __launch_bounds__(kEsThreads)
   }
 }
 
+template <typename TI>
+__global__ void __cluster_dims__(kEsCluster, 1, 1) __launch_bounds__(kEsThreads)
+    embed_sort_kernel(const TI* __restrict__ ids, uint32_t T, uint32_t V, int64_t padding_id, int passes, int digit_bits,
+                      uint32_t chunk, EmbedSort p) {
+  __shared__ uint32_t hist[kEsWarps][kEsBins];  // counts, then next output positions
+  grid_dependents_launch();  // the zeros need only the ids; the sums wait for this grid
+  embed_sort(hist, ids, T, V, padding_id, passes, digit_bits, chunk, p);
+}
+
+// Zeros in the rows of the table that no token names: CTA z takes a contiguous
+// range of rows, whose bits it sets from the whole list of tokens. Launched
+// with programmatic serialisation it runs beside the sort, whose results it does
+// not use; it waits for it at its end, so that what follows this grid follows both.
+template <typename TI, typename TT, int E>
+__global__ void __launch_bounds__(kEsThreads)
+    embed_zero_kernel(const TI* __restrict__ ids, uint32_t T, uint32_t V, int64_t padding_id, TT* __restrict__ dtable,
+                      int64_t D) {
+  __shared__ uint32_t bits[kEzRows / 32];
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t z = blockIdx.x, nz = gridDim.x;
+  grid_dependents_launch();
+  const uint32_t v_end = static_cast<uint32_t>(V * (z + 1) / nz);
+  for (uint32_t v0 = static_cast<uint32_t>(V * z / nz); v0 < v_end; v0 += kEzRows) {
+    const uint32_t rows = min(v_end - v0, static_cast<uint32_t>(kEzRows));
+    for (uint32_t i = tid; i < (rows + 31) / 32; i += kEsThreads) bits[i] = 0u;
+    __syncthreads();
+#pragma unroll 8
+    for (uint32_t i = tid; i < T; i += kEsThreads) {
+      const uint32_t k = embed_key(ids, i, V, padding_id) - v0;
+      if (k < rows) atomicOr(&bits[k >> 5], 1u << (k & 31));
+    }
+    __syncthreads();
+    const float zero[E] = {};
+    for (uint32_t r = warp; r < rows; r += kEsWarps) {
+      if ((bits[r >> 5] >> (r & 31)) & 1u) continue;
+      TT* row = dtable + static_cast<int64_t>(v0 + r) * D;
+#pragma unroll 4
+      for (int64_t k = static_cast<int64_t>(lane) * E; k < D; k += 32 * E) Elem<TT, E>::store(row + k, zero);
+    }
+    __syncthreads();  // the bits are read
+  }
+  grid_dependency_wait();
+}
+
 // ---------------------------------------------------------------------------
 // The sums. Warp (chunk c, column tile): the segments that start in chunk c,
 // and chunk c's share of the long ones. part: fp32 rows, [2 c] for a long
 // segment that began in an earlier chunk, [2 c + 1] for one that begins here.
+// Rows of dy are read as they come in the list, 4 KB of them in flight per warp.
 constexpr int kEgWarps = 8;
-constexpr int kEgCols = 256;  // columns per warp
-constexpr int kEgBatch = 8;   // rows of dy in flight per warp
+constexpr int kEgCols = 256;   // columns per warp
+constexpr int kEgChunk = 32;   // sorted positions per warp
+constexpr int kEgShort = 8;    // ... of a list so short that chunks of 32 leave SMs without work
 
-template <typename TG, typename TT, int E, bool ACC>
-__global__ void __launch_bounds__(kEgWarps * 32)
-    embed_grad_kernel(const uint32_t* __restrict__ key, const uint32_t* __restrict__ val,
-                      const uint32_t* __restrict__ touched, const TG* __restrict__ dy, TT* __restrict__ dtable,
-                      float* __restrict__ part, uint32_t T, uint32_t V, int64_t D, float scale, uint32_t sum_blocks) {
+// the row as loaded, unpacked when it is added
+template <typename T, int E>
+struct EgRow {
+  static constexpr int NC = kEgCols / (32 * E);
+  float f[NC][E];
+  __device__ __forceinline__ void load(const T* row, int64_t col, int64_t D) {
+#pragma unroll
+    for (int u = 0; u < NC; ++u)
+      if (col + u * 32 * E < D) Elem<T, E>::load(row + col + u * 32 * E, f[u]);
+  }
+  __device__ __forceinline__ void add(float (&acc)[NC][E]) const {
+#pragma unroll
+    for (int u = 0; u < NC; ++u)
+#pragma unroll
+      for (int j = 0; j < E; ++j) acc[u][j] += f[u][j];
+  }
+};
+template <>
+struct EgRow<uint16_t, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* row, int64_t col, int64_t D) {
+    if (col < D)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "l"(row + col));
+  }
+  __device__ __forceinline__ void add(float (&acc)[1][8]) const {
+    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc[0][2 * j] += __uint_as_float(h[j] << 16);
+      acc[0][2 * j + 1] += __uint_as_float(h[j] & 0xFFFF0000u);
+    }
+  }
+};
+
+template <typename TG, typename TT, int E, int CH, bool ACC>
+__global__ void __launch_bounds__(kEgWarps * 32, 3)
+    embed_grad_kernel(const uint32_t* __restrict__ key, const uint32_t* __restrict__ val, const TG* __restrict__ dy,
+                      TT* __restrict__ dtable, float* __restrict__ part, uint32_t T, uint32_t V, int64_t D, float scale) {
   constexpr int NC = kEgCols / (32 * E);  // accesses per lane
+  constexpr uint32_t BATCH = E == 8 && sizeof(TG) == 2 ? 8 : 4;  // rows in flight
+  constexpr uint32_t kAll = 0xffffffffu;
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t tiles = static_cast<uint32_t>((D + kEgCols - 1) / kEgCols);
-  if (blockIdx.x >= sum_blocks) {
-    // zero rows: 32 rows of the table per warp and step
-    if constexpr (!ACC) {
-      const uint64_t nw = static_cast<uint64_t>(gridDim.x - sum_blocks) * kEgWarps;
-      const float z[E] = {};
-      for (uint64_t v = static_cast<uint64_t>(blockIdx.x - sum_blocks) * kEgWarps + warp; v < V; v += nw) {
-        if ((touched[v >> 5] >> (v & 31)) & 1u) continue;
-        for (int64_t k = static_cast<int64_t>(lane) * E; k < D; k += 32 * E)
-          Elem<TT, E>::store(dtable + static_cast<int64_t>(v) * D + k, z);
-      }
-    }
-    return;
-  }
-  const uint64_t item = static_cast<uint64_t>(blockIdx.x) * kEgWarps + warp;
-  const uint32_t c = static_cast<uint32_t>(item / tiles);
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const uint32_t item = blockIdx.x * kEgWarps + warp, c = item / tiles;
   const int64_t col = static_cast<int64_t>(item % tiles) * kEgCols + lane * E;
-  const uint32_t p0 = c * kEgChunk;
+  const uint32_t p0 = c * CH;
   if (p0 >= T) return;
 
-  const uint32_t ka = p0 + lane < T ? key[p0 + lane] : V;
-  if (__shfl_sync(0xffffffffu, ka, 0) == V) return;  // nothing but tokens that take no part
-  const uint32_t q = p0 + kEgChunk;
-  const uint32_t kb = q + lane < T ? key[q + lane] : V;
-  const uint32_t va = ka != V ? val[p0 + lane] : 0u, vb = kb != V ? val[q + lane] : 0u;
-  const uint32_t next = q + kEgChunk < T ? key[q + kEgChunk] : V;  // the first key two chunks on
-  const uint32_t first = __shfl_sync(0xffffffffu, ka, 0), last = __shfl_sync(0xffffffffu, ka, 31);
-  const uint32_t after = __shfl_sync(0xffffffffu, kb, 0);
-  const bool goes_on = last != V && after == last;
+  // lanes 0 .. CH - 1: the chunk's positions (ka, va) and the next chunk's (kb, vb)
+  const uint32_t q = p0 + CH;
+  const bool in_a = lane < CH && p0 + lane < T, in_b = lane < CH && q + lane < T;
+  const uint32_t ka = in_a ? key[p0 + lane] : V, kb = in_b ? key[q + lane] : V;
+  const uint32_t va = in_a ? val[p0 + lane] : 0u, vb = in_b ? val[q + lane] : 0u;
+  const uint32_t next = q + CH < T ? key[q + CH] : V;  // the first key two chunks on
+  const uint32_t before = p0 > 0 ? key[p0 - 1] : V;    // the last key of the chunk before
+  const uint32_t before2 = p0 > CH ? key[p0 - CH - 1] : V;  // ... and of the one before that
+  const uint32_t first = __shfl_sync(kAll, ka, 0), last = __shfl_sync(kAll, ka, CH - 1);
+  if (first == V) return;  // nothing but tokens that take no part
+  const bool goes_on = last != V && __shfl_sync(kAll, kb, 0) == last;
 
   uint32_t begin = 0;  // positions within [chunk | next chunk]
   bool head = false;   // the first segment belongs to partial row 2 c
-  if (p0 > 0 && key[p0 - 1] == first) {
-    const bool whole = first == last;
-    head = (whole && goes_on) || (p0 > kEgChunk && key[p0 - kEgChunk - 1] == first);
+  if (before == first) {
+    head = (first == last && goes_on) || before2 == first;
     // otherwise the warp of the chunk before finishes this segment
-    if (!head) begin = __popc(__ballot_sync(0xffffffffu, ka == first));
+    if (!head) begin = __popc(__ballot_sync(kAll, in_a && ka == first));
   }
-  uint32_t end = __popc(__ballot_sync(0xffffffffu, ka != V));
+  uint32_t end = __popc(__ballot_sync(kAll, in_a && ka != V));
   bool tail = false;  // the last segment belongs to partial row 2 c + 1
   if (goes_on && !(head && first == last)) {
     tail = next == last;
-    if (!tail && begin < 32) end += __popc(__ballot_sync(0xffffffffu, kb == last));
+    if (!tail) end += __popc(__ballot_sync(kAll, in_b && kb == last));
   }
   if (begin >= end) return;
 
-  auto key_of = [&](uint32_t i) { return __shfl_sync(0xffffffffu, i < 32 ? ka : kb, i & 31); };
-  auto val_of = [&](uint32_t i) { return __shfl_sync(0xffffffffu, i < 32 ? va : vb, i & 31); };
+  auto key_of = [&](uint32_t i) { return __shfl_sync(kAll, i < CH ? ka : kb, i < CH ? i : i - CH); };
+  auto val_of = [&](uint32_t i) { return __shfl_sync(kAll, i < CH ? va : vb, i < CH ? i : i - CH); };
   float acc[NC][E] = {};
   uint32_t cur = key_of(begin);
   auto flush = [&](float* prow) {
@@ -290,19 +404,15 @@ __global__ void __launch_bounds__(kEgWarps * 32)
     }
   };
   float* head_row = part + (2 * static_cast<int64_t>(c)) * D;
-  for (uint32_t i0 = begin; i0 < end; i0 += kEgBatch) {
-    float f[kEgBatch][NC][E];
+  for (uint32_t i0 = begin; i0 < end; i0 += BATCH) {
+    EgRow<TG, E> row[BATCH];
 #pragma unroll
-    for (int b = 0; b < kEgBatch; ++b) {
+    for (uint32_t b = 0; b < BATCH; ++b) {
       const uint32_t t = val_of(min(i0 + b, end - 1));
-#pragma unroll
-      for (int u = 0; u < NC; ++u) {
-        const int64_t k = col + u * 32 * E;
-        if (i0 + b < end && k < D) Elem<TG, E>::load(dy + static_cast<int64_t>(t) * D + k, f[b][u]);
-      }
+      if (i0 + b < end) row[b].load(dy + static_cast<int64_t>(t) * D, col, D);
     }
 #pragma unroll
-    for (int b = 0; b < kEgBatch; ++b) {
+    for (uint32_t b = 0; b < BATCH; ++b) {
       if (i0 + b >= end) break;
       const uint32_t kk = key_of(i0 + b);
       if (kk != cur) {
@@ -310,46 +420,86 @@ __global__ void __launch_bounds__(kEgWarps * 32)
         head = false;
         cur = kk;
       }
-#pragma unroll
-      for (int u = 0; u < NC; ++u)
-#pragma unroll
-        for (int j = 0; j < E; ++j) acc[u][j] += f[b][u][j];
+      row[b].add(acc);
     }
   }
   flush(head ? head_row : tail ? head_row + D : nullptr);
 }
 
-// One CTA per (long segment, 32 columns), grid-stride: its partial rows added
-// in order, the warps taking contiguous shares.
-template <typename TT, bool ACC>
+// The long segments' partial rows added in order: a warp per (segment, 32 E
+// columns) where they are few, a CTA where they are many, each of its warps a
+// contiguous share.
+constexpr uint32_t kEhFew = 32;
+
+template <typename TT, int E, bool ACC>
 __global__ void __launch_bounds__(kEgWarps * 32)
     embed_grad_heavy_kernel(const uint32_t* __restrict__ key, const uint32_t* __restrict__ num_heavy,
                             const EmbedHeavy* __restrict__ heavy, const float* __restrict__ part,
-                            TT* __restrict__ dtable, int64_t D, float scale) {
-  __shared__ float sh[kEgWarps][32];
+                            TT* __restrict__ dtable, uint32_t chunk, int64_t D, float scale) {
+  __shared__ float sh[kEgWarps][32 * E];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t tiles = static_cast<uint32_t>((D + 31) / 32);
-  const uint64_t items = static_cast<uint64_t>(*num_heavy) * tiles;
+  const uint32_t tiles = static_cast<uint32_t>((D + 32 * E - 1) / (32 * E));
+  grid_dependency_wait();
+  const uint32_t n = *num_heavy;
+  // sum of partial rows a .. b of a segment that began in chunk `first`
+  auto add_rows = [&](uint32_t first, uint32_t a, uint32_t b, int64_t k, float(&t)[E]) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) t[j] = 0.f;
+    if (k >= D) return;
+    for (uint32_t c0 = a; c0 < b; c0 += 4) {
+      float f[4][E];
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t c = c0 + i;
+        if (c < b) {
+          Elem<float, E>::load(part + (2 * static_cast<int64_t>(c) + (c == first ? 1 : 0)) * D + k, f[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j) f[i][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < E; ++j) t[j] += f[i][j];
+    }
+  };
+  auto write = [&](const EmbedHeavy& s, int64_t k, const float(&t)[E]) {
+    if (k >= D) return;
+    TT* out = dtable + static_cast<int64_t>(key[static_cast<uint64_t>(s.last) * chunk]) * D + k;
+    float o[E];
+    if constexpr (ACC) Elem<TT, E>::load(out, o);
+#pragma unroll
+    for (int j = 0; j < E; ++j) o[j] = ACC ? fmaf(t[j], scale, o[j]) : t[j] * scale;
+    Elem<TT, E>::store(out, o);
+  };
+  float t[E];
+  const uint64_t items = static_cast<uint64_t>(n) * tiles;
+  for (uint64_t it = static_cast<uint64_t>(blockIdx.x) * kEgWarps + warp; it < items; it += gridDim.x * kEgWarps) {
+    const EmbedHeavy s = heavy[it / tiles];
+    if (s.last - s.first >= kEhFew) continue;
+    const int64_t k = static_cast<int64_t>(it % tiles) * (32 * E) + lane * E;
+    add_rows(s.first, s.first, s.last + 1, k, t);
+    write(s, k, t);
+  }
   for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const EmbedHeavy s = heavy[it / tiles];
-    const int64_t k = static_cast<int64_t>(it % tiles) * 32 + lane;
-    const uint32_t n = s.last - s.first + 1, per = (n + kEgWarps - 1) / kEgWarps;
-    const uint32_t a = s.first + min(n, warp * per), b = s.first + min(n, (warp + 1) * per);
-    float t = 0.f;
-    if (k < D)
-      for (uint32_t c = a; c < b; ++c) t += part[(2 * static_cast<int64_t>(c) + (c == s.first ? 1 : 0)) * D + k];
+    if (s.last - s.first < kEhFew) continue;  // uniform over the CTA
+    const int64_t k = static_cast<int64_t>(it % tiles) * (32 * E) + lane * E;
+    const uint32_t m = s.last - s.first + 1, per = (m + kEgWarps - 1) / kEgWarps;
+    add_rows(s.first, s.first + min(m, warp * per), s.first + min(m, (warp + 1) * per), k, t);
     __syncthreads();  // sh is still read from the item before
-    sh[warp][lane] = t;
-    __syncthreads();
-    if (warp == 0 && k < D) {
-      t = 0.f;
 #pragma unroll
-      for (int w = 0; w < kEgWarps; ++w) t += sh[w][lane];
-      TT* out = dtable + static_cast<int64_t>(key[s.last * kEgChunk]) * D + k;
-      float o[1] = {0.f};
-      if constexpr (ACC) Elem<TT, 1>::load(out, o);
-      o[0] = ACC ? fmaf(t, scale, o[0]) : t * scale;
-      Elem<TT, 1>::store(out, o);
+    for (int j = 0; j < E; ++j) sh[warp][j * 32 + lane] = t[j];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        t[j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kEgWarps; ++w) t[j] += sh[w][j * 32 + lane];
+      }
+      write(s, k, t);
     }
   }
 }

@@ -8,7 +8,8 @@
 // a double where it is far inside the range, and formed again in doubles
 // where it is not (rare, and exact enough at any scale). The CTAs' sums are
 // stored in order and added in order by every CTA of the second kernel, so the
-// norm does not depend on the order of execution.
+// norm does not depend on the order of execution. Both kernels are bound by
+// memory: all loads of a chunk are issued before the first is used.
 #pragma once
 
 #include "bl_elem.cuh"
@@ -16,55 +17,43 @@
 namespace bl {
 
 constexpr int kGcThreads = 256;
-constexpr int kGcVecs = 8;                           // 16-byte accesses per thread and chunk
-constexpr int kGcChunkVecs = kGcThreads * kGcVecs;   // a chunk is 32 KB of one tensor
-constexpr int kGcMaxTensors = 1024;                  // per launch: descriptors travel as kernel parameters
-constexpr int kGcMaxCtas = 1024;                     // partial sums per launch
+constexpr int kGcVecs = 4;                           // 16-byte accesses per thread and chunk
+constexpr int kGcChunkVecs = kGcThreads * kGcVecs;   // a chunk is 16 KB of one tensor
+constexpr int kGcMaxTensors = 900;                   // per launch: descriptors travel as kernel parameters
+constexpr int kGcMaxCtas = 1184;                     // partial sums per launch
 
 struct GcTensor {
   const void* g;
   void* out;
   int64_t numel;
 };
+// CTA b takes chunks [n b / grid, n (b + 1) / grid). Parameters are read through
+// the constant cache, a miss at a time: the tensor of a CTA's first chunk is
+// looked up by the host (a search over the table took longer than the sums of a
+// small model).
 template <int CAP>
 struct GcParams {
   GcTensor t[CAP];
-  int32_t chunk0[CAP + 1];  // first chunk of each tensor
+  int32_t chunk0[CAP + 1];     // first chunk of each tensor
+  uint16_t first[kGcMaxCtas + 1];  // tensor of chunk n b / grid
   uint8_t f32[CAP];
-  int32_t n;
 };
 
-// tensor of chunk c: the last one that starts at or before it
-template <int CAP>
-__device__ __forceinline__ int gc_find(const GcParams<CAP>& P, int c) {
-  int lo = 0, hi = P.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (P.chunk0[mid] <= c)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
+__host__ __device__ inline int gc_begin(int chunks, int b, int grid) {
+  return static_cast<int>(static_cast<int64_t>(chunks) * b / grid);
 }
 
 template <typename T>
-__device__ __forceinline__ float gc_value(uint32_t word, int j);
-template <>
-__device__ __forceinline__ float gc_value<float>(uint32_t word, int) {
-  return __uint_as_float(word);
-}
-template <>
-__device__ __forceinline__ float gc_value<uint16_t>(uint32_t word, int j) {
+__device__ __forceinline__ float gc_value(uint32_t word, int j) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(word);
   return j == 0 ? __uint_as_float(word << 16) : __uint_as_float(word & 0xFFFF0000u);
 }
 
-// sum of squares of one 16-byte access
+// squares of one 16-byte access added in fp32; `good` unless that may have left the range
 template <typename T>
-__device__ __forceinline__ double gc_squares(const uint4& v) {
+__device__ __forceinline__ float gc_squares(const uint4& v, bool& good) {
   constexpr int PER = 4 / sizeof(T);
   const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-  if (((v.x | v.y | v.z | v.w) & (sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0u) return 0.0;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -74,7 +63,14 @@ __device__ __forceinline__ double gc_squares(const uint4& v) {
       s = fmaf(f, f, s);
     }
   // 2^-60: a square lost below the smallest normal, 2^-126, is nothing next to it
-  if (s > 0x1p-60f && s < 0x1p120f) return static_cast<double>(s);
+  const uint32_t any = (v.x | v.y | v.z | v.w) & (sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
+  good = good && ((s > 0x1p-60f && s < 0x1p120f) || any == 0u);
+  return s;
+}
+template <typename T>
+__device__ __noinline__ double gc_squares_exact(uint4 v) {
+  constexpr int PER = 4 / sizeof(T);
+  const uint32_t h[4] = {v.x, v.y, v.z, v.w};
   double t = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -86,38 +82,69 @@ __device__ __forceinline__ double gc_squares(const uint4& v) {
   return t;
 }
 
-// f(first element, number of elements): the 16-byte aligned pieces of chunk
-// `rel` of a tensor; pieces cut by the tensor's ends are shorter. The pieces
-// are counted from the aligned address at or below the tensor's first byte.
-template <typename T, typename Whole, typename Cut>
-__device__ __forceinline__ void gc_for_chunk(const void* g, int64_t numel, int rel, Whole&& whole, Cut&& cut) {
-  constexpr int PER = 16 / sizeof(T);
-  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / sizeof(T));
-  const int64_t v0 = static_cast<int64_t>(rel) * kGcChunkVecs + threadIdx.x;
-#pragma unroll
-  for (int u = 0; u < kGcVecs; ++u) {
-    const int64_t e = (v0 + u * kGcThreads) * PER - mis;
-    if (e >= 0 && e + PER <= numel)
-      whole(u, e);
-    else if (e < numel && e + PER > 0)
-      cut(e < 0 ? 0 : e, e + PER < numel ? e + PER : numel);
+// A thread's share of chunk `rel` of a tensor: the 16-byte pieces v0 + u *
+// kGcThreads, counted from the aligned address at or below the tensor's first
+// byte, so piece v begins at element v * PER - mis. Pieces that lie within the
+// tensor are accessed whole; those that its ends cut (two at most) element by
+// element, by the one thread that has them.
+template <typename T>
+struct GcShare {
+  static constexpr int PER = 16 / sizeof(T);
+  int64_t e0;  // first element of piece 0
+  int64_t numel;
+  __device__ __forceinline__ GcShare(const GcTensor& t, int rel) {
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(t.g) & 15u) / sizeof(T));
+    e0 = (static_cast<int64_t>(rel) * kGcChunkVecs + threadIdx.x) * PER - mis;
+    numel = t.numel;
   }
+  __device__ __forceinline__ int64_t at(int u) const { return e0 + u * (kGcThreads * PER); }
+  __device__ __forceinline__ bool whole(int u) const { return at(u) >= 0 && at(u) + PER <= numel; }
+  // f(first element, end) of the pieces that the ends cut
+  template <typename F>
+  __device__ __forceinline__ void cut(F&& f) const {
+    if (e0 >= 0 && at(kGcVecs - 1) + PER <= numel) return;
+#pragma unroll 1
+    for (int u = 0; u < kGcVecs; ++u) {
+      const int64_t e = at(u);
+      if (!whole(u) && e < numel && e + PER > 0) f(e < 0 ? 0 : e, e + PER < numel ? e + PER : numel);
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 gc_load(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
 template <typename T>
 __device__ __forceinline__ double gc_norm_chunk(const GcTensor& t, int rel) {
   const T* g = static_cast<const T*>(t.g);
+  const GcShare<T> sh(t, rel);
+  uint4 v[kGcVecs];
+#pragma unroll
+  for (int u = 0; u < kGcVecs; ++u) v[u] = sh.whole(u) ? gc_load(g + sh.at(u)) : make_uint4(0u, 0u, 0u, 0u);
+  bool good = true;
+  float f[kGcVecs];
+#pragma unroll
+  for (int u = 0; u < kGcVecs; ++u) f[u] = gc_squares<T>(v[u], good);
   double s = 0.0;
-  gc_for_chunk<T>(
-      t.g, t.numel, rel,
-      [&](int, int64_t e) { s += gc_squares<T>(*reinterpret_cast<const uint4*>(g + e)); },
-      [&](int64_t a, int64_t b) {
-        for (int64_t i = a; i < b; ++i) {
-          float f[1];
-          Elem<T, 1>::load(g + i, f);
-          s = fma(static_cast<double>(f[0]), static_cast<double>(f[0]), s);
-        }
-      });
+  if (good) {
+#pragma unroll
+    for (int u = 0; u < kGcVecs; u += 2) s += static_cast<double>(f[u]) + static_cast<double>(f[u + 1]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kGcVecs; ++u) s += gc_squares_exact<T>(v[u]);
+  }
+  sh.cut([&](int64_t a, int64_t b) {
+    for (int64_t i = a; i < b; ++i) {
+      float e[1];
+      Elem<T, 1>::load(g + i, e);
+      s = fma(static_cast<double>(e[0]), static_cast<double>(e[0]), s);
+    }
+  });
   return s;
 }
 
@@ -133,14 +160,13 @@ __device__ __forceinline__ double gc_block_sum(double v, double* sh) {
 
 template <int CAP>
 __global__ void __launch_bounds__(kGcThreads)
-    grad_norm_kernel(const __grid_constant__ GcParams<CAP> P, double* __restrict__ sums) {
+    grad_norm_kernel(const __grid_constant__ GcParams<CAP> P, int chunks, double* __restrict__ sums) {
   __shared__ double sh[kGcThreads / 32];
-  const int chunks = P.chunk0[P.n];
-  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * blockIdx.x / gridDim.x);
-  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (blockIdx.x + 1) / gridDim.x);
+  const int c0 = gc_begin(chunks, blockIdx.x, gridDim.x), c1 = gc_begin(chunks, blockIdx.x + 1, gridDim.x);
+  grid_dependents_launch();  // the next kernel may be scheduled; it waits for the sums
   double s = 0.0;
   if (c0 < c1) {
-    int i = gc_find(P, c0);
+    int i = P.first[blockIdx.x];
     for (int c = c0; c < c1; ++c) {
       while (P.chunk0[i + 1] <= c) ++i;
       const int rel = c - P.chunk0[i];
@@ -165,32 +191,46 @@ __device__ __forceinline__ void gc_scale_chunk(const GcTensor& t, int rel, float
       Elem<T, 1>::store(out + i, f);
     }
   };
-  gc_for_chunk<T>(
-      t.g, t.numel, rel,
-      [&](int, int64_t e) {
-        if (!same) return single(e, e + PER);
-        const uint4 v = *reinterpret_cast<const uint4*>(g + e);
-        uint32_t h[4] = {v.x, v.y, v.z, v.w};
+  const GcShare<T> sh(t, rel);
+  uint4 v[kGcVecs];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (sizeof(T) == 4) {
-            h[i] = __float_as_uint(__uint_as_float(h[i]) * coef);
-          } else {
-            h[i] = static_cast<uint32_t>(float_to_bf16_bits(gc_value<T>(h[i], 0) * coef)) |
-                   (static_cast<uint32_t>(float_to_bf16_bits(gc_value<T>(h[i], 1) * coef)) << 16);
-          }
-        }
-        *reinterpret_cast<uint4*>(out + e) = make_uint4(h[0], h[1], h[2], h[3]);
-      },
-      single);
+  for (int u = 0; u < kGcVecs; ++u) v[u] = sh.whole(u) ? gc_load(g + sh.at(u)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int u = 0; u < kGcVecs; ++u) {
+    uint32_t h[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        h[i] = __float_as_uint(__uint_as_float(h[i]) * coef);
+      } else {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(gc_value<T>(h[i], 0) * coef, gc_value<T>(h[i], 1) * coef);
+        h[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    if (!sh.whole(u)) continue;
+    T* o = out + sh.at(u);
+    if (same) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[1], h[2], h[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        if constexpr (sizeof(T) == 4)
+          o[j] = __uint_as_float(h[j]);
+        else
+          o[j] = static_cast<uint16_t>(h[j / 2] >> (16 * (j & 1)));
+      }
+    }
+  }
+  sh.cut(single);
 }
 
 // stats[0] = norm, stats[1] = coefficient; then the tensors of this launch
 template <int CAP>
 __global__ void __launch_bounds__(kGcThreads)
-    grad_scale_kernel(const __grid_constant__ GcParams<CAP> P, const double* __restrict__ sums, int num_sums,
-                      float max_norm, float* __restrict__ stats) {
+    grad_scale_kernel(const __grid_constant__ GcParams<CAP> P, int chunks, const double* __restrict__ sums,
+                      int num_sums, float max_norm, float* __restrict__ stats) {
   __shared__ double sh[kGcThreads / 32];
+  grid_dependency_wait();
   double s = 0.0;
   for (int i = threadIdx.x; i < num_sums; i += kGcThreads) s += sums[i];
   const double norm = sqrt(gc_block_sum(s, sh));
@@ -201,11 +241,10 @@ __global__ void __launch_bounds__(kGcThreads)
     stats[0] = static_cast<float>(norm);
     stats[1] = coef;
   }
-  const int chunks = P.chunk0[P.n];
-  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * blockIdx.x / gridDim.x);
-  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (blockIdx.x + 1) / gridDim.x);
+  const int c0 = gc_begin(chunks, blockIdx.x, gridDim.x), c1 = gc_begin(chunks, blockIdx.x + 1, gridDim.x);
   if (c0 >= c1) return;
-  int i = gc_find(P, c1 - 1);
+  // from the last chunk down: what the norm's pass read last is still in L2
+  int i = P.first[blockIdx.x + 1];
   for (int ch = c1 - 1; ch >= c0; --ch) {
     while (P.chunk0[i] > ch) --i;
     const GcTensor& t = P.t[i];

@@ -205,6 +205,15 @@ def test_one_workspace_for_calls_in_a_row(bl):
         assert torch.equal(got.cpu(), torch.zeros(V, 64).index_add_(0, ids, dy))
 
 
+def test_workspace_on_any_16_byte_boundary(bl):
+    need = bl.workspace_bytes(bl.BL_OP_EMBEDDING_BACKWARD, 3000, 50, 64)
+    buf = torch.empty(need + 64, dtype=torch.uint8, device="cuda")
+    ids, dy = _zipf(3000, 50, 5), torch.randint(-4, 5, (3000, 64), generator=_gen(6)).float()
+    ref = torch.zeros(50, 64).index_add_(0, ids, dy)
+    for off in (0, 16, 48):
+        assert torch.equal(bl.embedding_backward(ids.cuda(), dy.cuda(), 50, ws=buf[off:off + need]).cpu(), ref)
+
+
 def test_two_streams_and_a_graph(bl):
     T, V, D = 3000, 2000, 128
     data = [(_zipf(T, V, s).cuda(), torch.randint(-4, 5, (T, D), generator=_gen(s)).to(BF16).cuda()) for s in (1, 2)]
