@@ -567,7 +567,7 @@ NormWs norm_ws(int64_t M, int64_t K) {
 
 struct EmbedWs {
   int64_t chunk, chunks;  // sorted positions per warp of the sums
-  size_t key[2], val[2], num_heavy, heavy, part, bytes;
+  size_t list[2], num_heavy, heavy, part, bytes;
 };
 EmbedWs embed_ws(int64_t T, int64_t V, int64_t D) {
   EmbedWs w{};
@@ -581,11 +581,8 @@ EmbedWs embed_ws(int64_t T, int64_t V, int64_t D) {
     at += align256(bytes);
     return a;
   };
-  for (int i = 0; i < 2; ++i) {
-    w.key[i] = take(size_t(T) * 4);
-    w.val[i] = take(size_t(T) * 4);
-  }
-  w.num_heavy = take(4);
+  for (int i = 0; i < 2; ++i) w.list[i] = take(size_t(T) * sizeof(uint2));
+  w.num_heavy = take(8);
   w.heavy = take(size_t(w.chunks) * sizeof(EmbedHeavy));
   w.part = take(size_t(2 * w.chunks) * size_t(D) * 4);
   w.bytes = at + 256;  // the sections begin at the first 256-byte boundary
@@ -1309,20 +1306,17 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
   if (rc != BL_OK) return rc;
   uint8_t* base = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(ws)));
   EmbedSort p;
-  for (int i = 0; i < 2; ++i) {
-    p.key[i] = reinterpret_cast<uint32_t*>(base + w.key[i]);
-    p.val[i] = reinterpret_cast<uint32_t*>(base + w.val[i]);
-  }
+  for (int i = 0; i < 2; ++i) p.list[i] = reinterpret_cast<uint2*>(base + w.list[i]);
   p.num_heavy = reinterpret_cast<uint32_t*>(base + w.num_heavy);
   p.heavy = reinterpret_cast<EmbedHeavy*>(base + w.heavy);
+  p.room = static_cast<uint32_t>(w.chunks);
   float* part = reinterpret_cast<float*>(base + w.part);
   // keys are 0 .. V: equal digits of at most 8 bits
   int bits = 1;
   while ((V >> bits) != 0) ++bits;
   const int passes = (bits + 7) / 8, digit_bits = (bits + passes - 1) / passes;
   const uint32_t t32 = static_cast<uint32_t>(T), v32 = static_cast<uint32_t>(V);
-  const uint32_t* key = p.key[(passes + 1) & 1];
-  const uint32_t* val = p.val[(passes + 1) & 1];
+  const uint2* list = p.list[(passes + 1) & 1];
   // writers of zeros: a CTA on each SM that does not sort, and rows for each of its warps
   const unsigned zero_grid = static_cast<unsigned>(std::min<int64_t>(cdiv(V, kEsWarps), std::max(1, sms - kEsCluster)));
   const unsigned sum_grid = static_cast<unsigned>(cdiv(w.chunks * cdiv(D, kEgCols), kEgWarps));
@@ -1330,8 +1324,12 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
   const bool vec = rows_vec(dy, dy_type, D, D, 1) && rows_vec(dtable, table_type, D, D, 1);
   auto sort = [&](auto ti) {
     using TI = decltype(ti);
-    embed_sort_kernel<TI><<<kEsCluster, kEsThreads, 0, s>>>(static_cast<const TI*>(ids), t32, v32, padding_id, passes,
-                                                            digit_bits, chunk, p);
+    const auto* id = static_cast<const TI*>(ids);
+    if (T <= kEsOneCta)
+      embed_sort_kernel<TI, 1><<<1, kEsThreads, 0, s>>>(id, t32, v32, padding_id, passes, digit_bits, chunk, p);
+    else
+      embed_sort_kernel<TI, kEsCluster><<<kEsCluster, kEsThreads, 0, s>>>(id, t32, v32, padding_id, passes, digit_bits,
+                                                                        chunk, p);
     return launch_status();
   };
   rc = id_type == BL_IDS_I64 ? sort(int64_t{}) : sort(int32_t{});
@@ -1353,14 +1351,15 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
       if (st != BL_OK) return st;
       constexpr auto by_32 = embed_grad_kernel<TG, TT, E, kEgChunk, ACC>;
       constexpr auto by_8 = embed_grad_kernel<TG, TT, E, kEgShort, ACC>;
-      st = launch_after(w.chunk == kEgChunk ? by_32 : by_8, dim3(sum_grid), kEgWarps * 32, 0, s, key, val,
+      st = launch_after(w.chunk == kEgChunk ? by_32 : by_8, dim3(sum_grid), kEgWarps * 32, 0, s, list,
                         static_cast<const TG*>(dy), out, part, t32, v32, D, scale);
       if (st != BL_OK || w.chunks < 3) return st;  // a long segment spans three chunks
-      constexpr int HE = E == 8 ? 8 : 1;
+      constexpr int HE = E == 8 ? 4 : 1;
       const int64_t most = cdiv((w.chunks / 2) * cdiv(D, 32 * HE), kEgWarps);
       return launch_after(embed_grad_heavy_kernel<TT, HE, ACC>, dim3(unsigned(std::min<int64_t>(most, int64_t(sms) * 4))),
-                          kEgWarps * 32, 0, s, key, static_cast<const uint32_t*>(p.num_heavy),
-                          static_cast<const EmbedHeavy*>(p.heavy), static_cast<const float*>(part), out, chunk, D, scale);
+                          kEgWarps * 32, 0, s, list, static_cast<const uint32_t*>(p.num_heavy),
+                          static_cast<const EmbedHeavy*>(p.heavy), p.room, static_cast<const float*>(part), out, chunk, D,
+                          scale);
     };
     using E1 = Int<1>;
     using E8 = Int<8>;

@@ -29,6 +29,11 @@ struct Elem<uint16_t, 2> {
 };
 template <>
 struct Elem<uint16_t, 4> {
+  static __device__ __forceinline__ void load(const uint16_t* p, float (&f)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
   static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[4]) {
     __nv_bfloat162 h[2] = {__floats2bfloat162_rn(f[0], f[1]), __floats2bfloat162_rn(f[2], f[3])};
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
@@ -36,6 +41,10 @@ struct Elem<uint16_t, 4> {
 };
 template <>
 struct Elem<float, 4> {
+  static __device__ __forceinline__ void load(const float* p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  }
   static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   }

@@ -75,6 +75,8 @@ constexpr int kEsCluster = 8;
 constexpr int kEsThreads = 1024;
 constexpr int kEsWarps = kEsThreads / 32;
 constexpr int kEsBins = 256;
+constexpr int kEsOneCta = 4096;  // positions up to which one CTA sorts alone
+constexpr uint32_t kEhFew = 16;  // a long segment's partial rows that one warp adds up
 constexpr int kEsHold = 8;    // positions per lane that are held between counting and placing
 constexpr int kEzRows = 8192 * 32;  // rows of the table whose bits fit the shared memory of a CTA
 
@@ -83,13 +85,15 @@ struct EmbedHeavy {
 };
 
 struct EmbedSort {
-  uint32_t* key[2];
-  uint32_t* val[2];
-  uint32_t* num_heavy;
+  uint2* list[2];       // (id, position); the two in one store: scattered stores are what bounds a pass
+  uint32_t* num_heavy;  // [0]: listed from the front, [1]: those over more than kEhFew chunks, from the back
   EmbedHeavy* heavy;
+  uint32_t room;        // entries of the list
 };
 
+template <int CL>
 __device__ __forceinline__ void cluster_barrier() {
+  if constexpr (CL == 1) return __syncthreads();
   asm volatile(
       "barrier.cluster.arrive.release;\n\t"
       "barrier.cluster.wait.acquire;" ::
@@ -109,7 +113,7 @@ __device__ __forceinline__ uint32_t embed_key(const TI* ids, uint32_t i, uint32_
   return id >= 0 && id < V && id != padding_id ? static_cast<uint32_t>(id) : V;
 }
 
-template <typename TI>
+template <typename TI, int CL>
 __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* __restrict__ ids, uint32_t T, uint32_t V,
                                            int64_t padding_id, int passes, int digit_bits, uint32_t chunk,
                                            const EmbedSort& p) {
@@ -118,20 +122,18 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
   __shared__ uint32_t wsum[kEsBins / 32];
   const uint32_t rank = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t gtid = rank * kEsThreads + tid;
-  constexpr uint32_t kAll = kEsCluster * kEsThreads;
+  constexpr uint32_t kAll = CL * kEsThreads;
   // whole warps of positions: a warp's run, then a CTA's
   const uint32_t run = ((T + kAll - 1) / kAll) * 32;
   const uint32_t w0 = min(T, (rank * kEsWarps + warp) * run), w1 = min(T, w0 + run);
   const bool hold = run <= kEsHold * 32;
-  if (gtid == 0) *p.num_heavy = 0u;
+  if (gtid < 2) p.num_heavy[gtid] = 0u;
   const uint32_t mask = (1u << digit_bits) - 1u;
 
   for (int pass = 0; pass < passes; ++pass) {
     const int shift = pass * digit_bits;
-    const uint32_t* kin = p.key[(pass + 1) & 1];
-    const uint32_t* vin = p.val[(pass + 1) & 1];
-    uint32_t* kout = p.key[pass & 1];
-    uint32_t* vout = p.val[pass & 1];
+    const uint2* in = p.list[(pass + 1) & 1];
+    uint2* out = p.list[pass & 1];
     uint32_t kh[kEsHold], vh[kEsHold];
     // the block of positions b0 + 32 u + lane (key V + 1: none)
     auto load = [&](uint32_t b0) {
@@ -140,8 +142,9 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
         const uint32_t i = b0 + 32 * u + lane;
         kh[u] = V + 1;
         if (i < w1) {
-          kh[u] = pass > 0 ? __ldcg(kin + i) : embed_key(ids, i, V, padding_id);
-          vh[u] = pass > 0 ? __ldcg(vin + i) : i;
+          const uint2 kv = pass > 0 ? __ldcg(in + i) : make_uint2(embed_key(ids, i, V, padding_id), i);
+          kh[u] = kv.x;
+          vh[u] = kv.y;
         }
       }
     };
@@ -175,15 +178,18 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
       all4 += x;
     }
     if (q == 0) tot[d] = all4;
-    cluster_barrier();
-    uint32_t below = 0, all = 0, inc = 0;
-    uint32_t x[kEsCluster];
+    uint32_t below = 0, all = all4, inc = 0;
+    if constexpr (CL > 1) {
+      cluster_barrier<CL>();
+      uint32_t x[CL];
 #pragma unroll
-    for (uint32_t r = 0; r < kEsCluster; ++r) x[r] = ld_cluster_u32(smem_u32(&tot[d]), r);
+      for (uint32_t r = 0; r < CL; ++r) x[r] = ld_cluster_u32(smem_u32(&tot[d]), r);
+      all = 0;
 #pragma unroll
-    for (uint32_t r = 0; r < kEsCluster; ++r) {
-      below += r < rank ? x[r] : 0u;
-      all += x[r];
+      for (uint32_t r = 0; r < CL; ++r) {
+        below += r < rank ? x[r] : 0u;
+        all += x[r];
+      }
     }
     // exclusive sum of `all` over the digits (the four quarters of the threads do the same)
     inc = all;
@@ -211,48 +217,53 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
           const int64_t id = static_cast<int64_t>(ids[vh[u]]);
           if (id < 0 || id >= V) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingGradId);
         }
-        const uint32_t same = __match_any_sync(0xffffffffu, dig);
+        // lanes with the same digit, one vote per bit
+        uint32_t same = __ballot_sync(0xffffffffu, live);
+        for (int b = 0; b < digit_bits; ++b) {
+          const bool bit = (dig >> b) & 1u;
+          const uint32_t votes = __ballot_sync(0xffffffffu, bit);
+          same &= bit ? votes : ~votes;
+        }
         const uint32_t before = __popc(same & ((1u << lane) - 1u));
         uint32_t at = 0;
         if (live) at = hist[warp][dig] + before;
         __syncwarp();
         if (live && before == 0) hist[warp][dig] += __popc(same);
         __syncwarp();
-        if (live) {
-          kout[at] = kh[u];
-          vout[at] = vh[u];
-        }
+        if (live) out[at] = make_uint2(kh[u], vh[u]);
       }
     }
-    cluster_barrier();  // the sorted list, and `tot` read by everyone
+    cluster_barrier<CL>();  // the sorted list, and `tot` read by everyone
   }
 
   // list the segments that reach past the chunk after the one they start in
-  const uint32_t* key = p.key[(passes + 1) & 1];
+  const uint2* list = p.list[(passes + 1) & 1];
   const uint32_t chunks = (T + chunk - 1) / chunk;
   for (uint32_t c = gtid; c + 2 < chunks; c += kAll) {
-    const uint32_t h = __ldcg(key + (c + 1) * chunk - 1);
-    if (h == V || __ldcg(key + (c + 2) * chunk) != h) continue;
-    if (c > 0 && __ldcg(key + c * chunk - 1) == h) continue;  // it started earlier
+    const uint32_t h = __ldcg(list + (c + 1) * chunk - 1).x;
+    if (h == V || __ldcg(list + (c + 2) * chunk).x != h) continue;
+    if (c > 0 && __ldcg(list + c * chunk - 1).x == h) continue;  // it started earlier
     uint32_t lo = c + 2, hi = chunks;  // chunk lo starts with h, chunk hi does not
     while (hi - lo > 1) {
       const uint32_t mid = lo + (hi - lo) / 2;
-      if (__ldcg(key + mid * chunk) == h)
+      if (__ldcg(list + mid * chunk).x == h)
         lo = mid;
       else
         hi = mid;
     }
-    p.heavy[atomicAdd(p.num_heavy, 1u)] = EmbedHeavy{c, lo};
+    const bool few = lo - c < kEhFew;
+    const uint32_t at = atomicAdd(p.num_heavy + (few ? 0 : 1), 1u);
+    p.heavy[few ? at : p.room - 1 - at] = EmbedHeavy{c, lo};
   }
 }
 
-template <typename TI>
-__global__ void __cluster_dims__(kEsCluster, 1, 1) __launch_bounds__(kEsThreads)
+template <typename TI, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kEsThreads)
     embed_sort_kernel(const TI* __restrict__ ids, uint32_t T, uint32_t V, int64_t padding_id, int passes, int digit_bits,
                       uint32_t chunk, EmbedSort p) {
   __shared__ uint32_t hist[kEsWarps][kEsBins];  // counts, then next output positions
   grid_dependents_launch();  // the zeros need only the ids; the sums wait for this grid
-  embed_sort(hist, ids, T, V, padding_id, passes, digit_bits, chunk, p);
+  embed_sort<TI, CL>(hist, ids, T, V, padding_id, passes, digit_bits, chunk, p);
 }
 
 // Zeros in the rows of the table that no token names: CTA z takes a contiguous
@@ -338,8 +349,8 @@ struct EgRow<uint16_t, 8> {
 
 template <typename TG, typename TT, int E, int CH, bool ACC>
 __global__ void __launch_bounds__(kEgWarps * 32, 3)
-    embed_grad_kernel(const uint32_t* __restrict__ key, const uint32_t* __restrict__ val, const TG* __restrict__ dy,
-                      TT* __restrict__ dtable, float* __restrict__ part, uint32_t T, uint32_t V, int64_t D, float scale) {
+    embed_grad_kernel(const uint2* __restrict__ list, const TG* __restrict__ dy, TT* __restrict__ dtable,
+                      float* __restrict__ part, uint32_t T, uint32_t V, int64_t D, float scale) {
   constexpr int NC = kEgCols / (32 * E);  // accesses per lane
   constexpr uint32_t BATCH = E == 8 && sizeof(TG) == 2 ? 8 : 4;  // rows in flight
   constexpr uint32_t kAll = 0xffffffffu;
@@ -355,11 +366,11 @@ __global__ void __launch_bounds__(kEgWarps * 32, 3)
   // lanes 0 .. CH - 1: the chunk's positions (ka, va) and the next chunk's (kb, vb)
   const uint32_t q = p0 + CH;
   const bool in_a = lane < CH && p0 + lane < T, in_b = lane < CH && q + lane < T;
-  const uint32_t ka = in_a ? key[p0 + lane] : V, kb = in_b ? key[q + lane] : V;
-  const uint32_t va = in_a ? val[p0 + lane] : 0u, vb = in_b ? val[q + lane] : 0u;
-  const uint32_t next = q + CH < T ? key[q + CH] : V;  // the first key two chunks on
-  const uint32_t before = p0 > 0 ? key[p0 - 1] : V;    // the last key of the chunk before
-  const uint32_t before2 = p0 > CH ? key[p0 - CH - 1] : V;  // ... and of the one before that
+  const uint2 none = make_uint2(V, 0u), pa = in_a ? list[p0 + lane] : none, pb = in_b ? list[q + lane] : none;
+  const uint32_t ka = pa.x, va = pa.y, kb = pb.x, vb = pb.y;
+  const uint32_t next = q + CH < T ? list[q + CH].x : V;       // the first key two chunks on
+  const uint32_t before = p0 > 0 ? list[p0 - 1].x : V;         // the last key of the chunk before
+  const uint32_t before2 = p0 > CH ? list[p0 - CH - 1].x : V;  // ... and of the one before that
   const uint32_t first = __shfl_sync(kAll, ka, 0), last = __shfl_sync(kAll, ka, CH - 1);
   if (first == V) return;  // nothing but tokens that take no part
   const bool goes_on = last != V && __shfl_sync(kAll, kb, 0) == last;
@@ -427,46 +438,41 @@ __global__ void __launch_bounds__(kEgWarps * 32, 3)
 }
 
 // The long segments' partial rows added in order: a warp per (segment, 32 E
-// columns) where they are few, a CTA where they are many, each of its warps a
+// columns) for those over few chunks, a CTA for the others, each of its warps a
 // contiguous share.
-constexpr uint32_t kEhFew = 32;
-
 template <typename TT, int E, bool ACC>
 __global__ void __launch_bounds__(kEgWarps * 32)
-    embed_grad_heavy_kernel(const uint32_t* __restrict__ key, const uint32_t* __restrict__ num_heavy,
-                            const EmbedHeavy* __restrict__ heavy, const float* __restrict__ part,
+    embed_grad_heavy_kernel(const uint2* __restrict__ list, const uint32_t* __restrict__ num_heavy,
+                            const EmbedHeavy* __restrict__ heavy, uint32_t room, const float* __restrict__ part,
                             TT* __restrict__ dtable, uint32_t chunk, int64_t D, float scale) {
   __shared__ float sh[kEgWarps][32 * E];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t tiles = static_cast<uint32_t>((D + 32 * E - 1) / (32 * E));
   grid_dependency_wait();
-  const uint32_t n = *num_heavy;
-  // sum of partial rows a .. b of a segment that began in chunk `first`
+  const uint64_t few = static_cast<uint64_t>(num_heavy[0]) * tiles, many = static_cast<uint64_t>(num_heavy[1]) * tiles;
+  // sum of partial rows a .. b - 1 of a segment that began in chunk `first`
   auto add_rows = [&](uint32_t first, uint32_t a, uint32_t b, int64_t k, float(&t)[E]) {
 #pragma unroll
     for (int j = 0; j < E; ++j) t[j] = 0.f;
     if (k >= D) return;
-    for (uint32_t c0 = a; c0 < b; c0 += 4) {
-      float f[4][E];
+    for (uint32_t c0 = a; c0 < b; c0 += 8) {
+      float f[8][E];
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
+      for (uint32_t i = 0; i < 8; ++i) {
         const uint32_t c = c0 + i;
-        if (c < b) {
-          Elem<float, E>::load(part + (2 * static_cast<int64_t>(c) + (c == first ? 1 : 0)) * D + k, f[i]);
-        } else {
 #pragma unroll
-          for (int j = 0; j < E; ++j) f[i][j] = 0.f;
-        }
+        for (int j = 0; j < E; ++j) f[i][j] = 0.f;
+        if (c < b) Elem<float, E>::load(part + (2 * static_cast<int64_t>(c) + (c == first ? 1 : 0)) * D + k, f[i]);
       }
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i)
+      for (uint32_t i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < E; ++j) t[j] += f[i][j];
     }
   };
   auto write = [&](const EmbedHeavy& s, int64_t k, const float(&t)[E]) {
     if (k >= D) return;
-    TT* out = dtable + static_cast<int64_t>(key[static_cast<uint64_t>(s.last) * chunk]) * D + k;
+    TT* out = dtable + static_cast<int64_t>(list[static_cast<uint64_t>(s.last) * chunk].x) * D + k;
     float o[E];
     if constexpr (ACC) Elem<TT, E>::load(out, o);
 #pragma unroll
@@ -474,17 +480,8 @@ __global__ void __launch_bounds__(kEgWarps * 32)
     Elem<TT, E>::store(out, o);
   };
   float t[E];
-  const uint64_t items = static_cast<uint64_t>(n) * tiles;
-  for (uint64_t it = static_cast<uint64_t>(blockIdx.x) * kEgWarps + warp; it < items; it += gridDim.x * kEgWarps) {
-    const EmbedHeavy s = heavy[it / tiles];
-    if (s.last - s.first >= kEhFew) continue;
-    const int64_t k = static_cast<int64_t>(it % tiles) * (32 * E) + lane * E;
-    add_rows(s.first, s.first, s.last + 1, k, t);
-    write(s, k, t);
-  }
-  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const EmbedHeavy s = heavy[it / tiles];
-    if (s.last - s.first < kEhFew) continue;  // uniform over the CTA
+  for (uint64_t it = blockIdx.x; it < many; it += gridDim.x) {
+    const EmbedHeavy s = heavy[room - 1 - it / tiles];
     const int64_t k = static_cast<int64_t>(it % tiles) * (32 * E) + lane * E;
     const uint32_t m = s.last - s.first + 1, per = (m + kEgWarps - 1) / kEgWarps;
     add_rows(s.first, s.first + min(m, warp * per), s.first + min(m, (warp + 1) * per), k, t);
@@ -501,6 +498,14 @@ __global__ void __launch_bounds__(kEgWarps * 32)
       }
       write(s, k, t);
     }
+  }
+  // from the last CTA down: the first ones have the long segments
+  const uint64_t me = static_cast<uint64_t>(gridDim.x - 1 - blockIdx.x) * kEgWarps + warp;
+  for (uint64_t it = me; it < few; it += static_cast<uint64_t>(gridDim.x) * kEgWarps) {
+    const EmbedHeavy s = heavy[it / tiles];
+    const int64_t k = static_cast<int64_t>(it % tiles) * (32 * E) + lane * E;
+    add_rows(s.first, s.first, s.last + 1, k, t);
+    write(s, k, t);
   }
 }
 
