@@ -238,6 +238,14 @@ __host__ __device__ constexpr uint32_t idesc_s8_s32(int m, int n) {
 // the dependents of this grid be scheduled
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Begin a kernel launched with programmatic serialisation that may follow, and
+// be followed by, any other: nothing is read before everything ahead of it is
+// complete, and only then may the next kernel be scheduled (one that prefetches
+// what an earlier kernel wrote, before its own wait, finds that written).
+__device__ __forceinline__ void grid_begin() {
+  grid_dependency_wait();
+  grid_dependents_launch();
+}
 
 // ---------------------------------------------------------------------------
 // misc

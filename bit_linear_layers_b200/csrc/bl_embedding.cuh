@@ -12,8 +12,9 @@
 // summed chunk by chunk into fp32 partial rows that a last kernel adds up in
 // order, so a token that fills the batch is as parallel as any other.
 // Most of the table's rows have no token, and zero-filling them is most of the
-// traffic: a second kernel writes zeros to the rows that no token names while
-// one cluster of eight SMs sorts, and each element of dE is written once.
+// traffic: the first CTAs of the second kernel write zeros to the rows that no
+// token names while one cluster of eight SMs sorts, the others wait for the list
+// and add up rows beside them. Each element of dE is written once.
 #pragma once
 
 #include "bl_elem.cuh"
@@ -38,6 +39,7 @@ __global__ void __launch_bounds__(kEmbThreads)
                      int64_t V, int64_t D, uint32_t tiles, float scale) {
   const uint32_t item = blockIdx.x * (kEmbThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t t = item / tiles, tile = item % tiles;
+  grid_begin();
   if (t >= T) return;
   const int64_t row = embed_row(ids, t, V);
   if (row < 0 && lane == 0 && tile == 0) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingId);
@@ -78,7 +80,6 @@ constexpr int kEsBins = 256;
 constexpr int kEsOneCta = 4096;  // positions up to which one CTA sorts alone
 constexpr uint32_t kEhFew = 16;  // a long segment's partial rows that one warp adds up
 constexpr int kEsHold = 8;    // positions per lane that are held between counting and placing
-constexpr int kEzRows = 8192 * 32;  // rows of the table whose bits fit the shared memory of a CTA
 
 struct EmbedHeavy {
   uint32_t first, last;  // the chunks in which a long segment starts and ends
@@ -134,7 +135,7 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
     const int shift = pass * digit_bits;
     const uint2* in = p.list[(pass + 1) & 1];
     uint2* out = p.list[pass & 1];
-    uint32_t kh[kEsHold], vh[kEsHold];
+    uint32_t kh[kEsHold], vh[kEsHold], same[kEsHold];
     // the block of positions b0 + 32 u + lane (key V + 1: none)
     auto load = [&](uint32_t b0) {
 #pragma unroll
@@ -147,14 +148,29 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
           vh[u] = kv.y;
         }
       }
+      // lanes with the same digit, one vote per bit (atomics on a frequent token's count take turns, up to 32
+      // of them)
+#pragma unroll
+      for (int u = 0; u < kEsHold; ++u) {
+        if (b0 + 32 * u >= w1) break;  // uniform over the warp
+        same[u] = __ballot_sync(0xffffffffu, kh[u] <= V);
+        for (int b = 0; b < digit_bits; ++b) {
+          const bool bit = (kh[u] >> (shift + b)) & 1u;
+          const uint32_t votes = __ballot_sync(0xffffffffu, bit);
+          same[u] &= bit ? votes : ~votes;
+        }
+      }
     };
     for (int d = lane; d < kEsBins; d += 32) hist[warp][d] = 0u;
     __syncwarp();
     for (uint32_t b0 = w0; b0 < w1; b0 += kEsHold * 32) {
       load(b0);
 #pragma unroll
-      for (int u = 0; u < kEsHold; ++u)
-        if (kh[u] <= V) atomicAdd(&hist[warp][(kh[u] >> shift) & mask], 1u);
+      for (int u = 0; u < kEsHold; ++u) {
+        if (b0 + 32 * u >= w1) break;
+        if (kh[u] <= V && (same[u] & ((1u << lane) - 1u)) == 0u) hist[warp][(kh[u] >> shift) & mask] += __popc(same[u]);
+        __syncwarp();
+      }
     }
     __syncthreads();
     // digit d: counts of the warps ahead, this CTA's total
@@ -212,23 +228,16 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
       for (int u = 0; u < kEsHold; ++u) {
         if (b0 + 32 * u >= w1) break;  // uniform over the warp
         const bool live = kh[u] <= V;
-        const uint32_t dig = live ? (kh[u] >> shift) & mask : kEsBins;
+        const uint32_t dig = (kh[u] >> shift) & mask;
         if (pass == 0 && kh[u] == V) {
           const int64_t id = static_cast<int64_t>(ids[vh[u]]);
           if (id < 0 || id >= V) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingGradId);
         }
-        // lanes with the same digit, one vote per bit
-        uint32_t same = __ballot_sync(0xffffffffu, live);
-        for (int b = 0; b < digit_bits; ++b) {
-          const bool bit = (dig >> b) & 1u;
-          const uint32_t votes = __ballot_sync(0xffffffffu, bit);
-          same &= bit ? votes : ~votes;
-        }
-        const uint32_t before = __popc(same & ((1u << lane) - 1u));
+        const uint32_t before = __popc(same[u] & ((1u << lane) - 1u));
         uint32_t at = 0;
         if (live) at = hist[warp][dig] + before;
         __syncwarp();
-        if (live && before == 0) hist[warp][dig] += __popc(same);
+        if (live && before == 0) hist[warp][dig] += __popc(same[u]);
         __syncwarp();
         if (live) out[at] = make_uint2(kh[u], vh[u]);
       }
@@ -262,35 +271,35 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kEsThreads)
     embed_sort_kernel(const TI* __restrict__ ids, uint32_t T, uint32_t V, int64_t padding_id, int passes, int digit_bits,
                       uint32_t chunk, EmbedSort p) {
   __shared__ uint32_t hist[kEsWarps][kEsBins];  // counts, then next output positions
-  grid_dependents_launch();  // the zeros need only the ids; the sums wait for this grid
+  grid_begin();  // what follows writes zeros meanwhile; its sums wait for this grid
   embed_sort<TI, CL>(hist, ids, T, V, padding_id, passes, digit_bits, chunk, p);
 }
 
-// Zeros in the rows of the table that no token names: CTA z takes a contiguous
-// range of rows, whose bits it sets from the whole list of tokens. Launched
-// with programmatic serialisation it runs beside the sort, whose results it does
-// not use; it waits for it at its end, so that what follows this grid follows both.
+// Zeros in the rows of the table that no token names: CTA z of nz takes a
+// contiguous range of rows, whose bits it sets from the whole list of tokens. It
+// uses nothing of the sort and does not wait for it.
+constexpr int kEgThreads = 256;
+constexpr int kEgWarps = kEgThreads / 32;
+constexpr int kEzRows = 4096 * 32;  // rows of the table whose bits are held at a time
+
 template <typename TI, typename TT, int E>
-__global__ void __launch_bounds__(kEsThreads)
-    embed_zero_kernel(const TI* __restrict__ ids, uint32_t T, uint32_t V, int64_t padding_id, TT* __restrict__ dtable,
-                      int64_t D) {
-  __shared__ uint32_t bits[kEzRows / 32];
+__device__ __forceinline__ void embed_zero(uint32_t* bits, const TI* __restrict__ ids, uint32_t T, uint32_t V,
+                                           int64_t padding_id, TT* __restrict__ dtable, int64_t D, uint64_t z,
+                                           uint64_t nz) {
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint64_t z = blockIdx.x, nz = gridDim.x;
-  grid_dependents_launch();
   const uint32_t v_end = static_cast<uint32_t>(V * (z + 1) / nz);
   for (uint32_t v0 = static_cast<uint32_t>(V * z / nz); v0 < v_end; v0 += kEzRows) {
     const uint32_t rows = min(v_end - v0, static_cast<uint32_t>(kEzRows));
-    for (uint32_t i = tid; i < (rows + 31) / 32; i += kEsThreads) bits[i] = 0u;
+    for (uint32_t i = tid; i < (rows + 31) / 32; i += kEgThreads) bits[i] = 0u;
     __syncthreads();
 #pragma unroll 8
-    for (uint32_t i = tid; i < T; i += kEsThreads) {
+    for (uint32_t i = tid; i < T; i += kEgThreads) {
       const uint32_t k = embed_key(ids, i, V, padding_id) - v0;
       if (k < rows) atomicOr(&bits[k >> 5], 1u << (k & 31));
     }
     __syncthreads();
     const float zero[E] = {};
-    for (uint32_t r = warp; r < rows; r += kEsWarps) {
+    for (uint32_t r = warp; r < rows; r += kEgWarps) {
       if ((bits[r >> 5] >> (r & 31)) & 1u) continue;
       TT* row = dtable + static_cast<int64_t>(v0 + r) * D;
 #pragma unroll 4
@@ -298,7 +307,6 @@ __global__ void __launch_bounds__(kEsThreads)
     }
     __syncthreads();  // the bits are read
   }
-  grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -306,7 +314,6 @@ __global__ void __launch_bounds__(kEsThreads)
 // and chunk c's share of the long ones. part: fp32 rows, [2 c] for a long
 // segment that began in an earlier chunk, [2 c + 1] for one that begins here.
 // Rows of dy are read as they come in the list, 4 KB of them in flight per warp.
-constexpr int kEgWarps = 8;
 constexpr int kEgCols = 256;   // columns per warp
 constexpr int kEgChunk = 32;   // sorted positions per warp
 constexpr int kEgShort = 8;    // ... of a list so short that chunks of 32 leave SMs without work
@@ -347,18 +354,26 @@ struct EgRow<uint16_t, 8> {
   }
 };
 
-template <typename TG, typename TT, int E, int CH, bool ACC>
-__global__ void __launch_bounds__(kEgWarps * 32, 3)
-    embed_grad_kernel(const uint2* __restrict__ list, const TG* __restrict__ dy, TT* __restrict__ dtable,
-                      float* __restrict__ part, uint32_t T, uint32_t V, int64_t D, float scale) {
+// The first `zero_ctas` CTAs write zeros. Launched with programmatic
+// serialisation: the zeros are written while the list is sorted.
+template <typename TI, typename TG, typename TT, int E, int CH, bool ACC>
+__global__ void __launch_bounds__(kEgThreads, 3)
+    embed_grad_kernel(const TI* __restrict__ ids, int64_t padding_id, uint32_t zero_ctas, const uint2* __restrict__ list,
+                      const TG* __restrict__ dy, TT* __restrict__ dtable, float* __restrict__ part, uint32_t T,
+                      uint32_t V, int64_t D, float scale) {
+  grid_dependents_launch();
+  if constexpr (!ACC) {
+    __shared__ uint32_t bits[kEzRows / 32];
+    if (blockIdx.x < zero_ctas)
+      return embed_zero<TI, TT, E>(bits, ids, T, V, padding_id, dtable, D, blockIdx.x, zero_ctas);
+  }
   constexpr int NC = kEgCols / (32 * E);  // accesses per lane
   constexpr uint32_t BATCH = E == 8 && sizeof(TG) == 2 ? 8 : 4;  // rows in flight
   constexpr uint32_t kAll = 0xffffffffu;
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t tiles = static_cast<uint32_t>((D + kEgCols - 1) / kEgCols);
-  grid_dependents_launch();
   grid_dependency_wait();
-  const uint32_t item = blockIdx.x * kEgWarps + warp, c = item / tiles;
+  const uint32_t item = (blockIdx.x - zero_ctas) * kEgWarps + warp, c = item / tiles;
   const int64_t col = static_cast<int64_t>(item % tiles) * kEgCols + lane * E;
   const uint32_t p0 = c * CH;
   if (p0 >= T) return;
@@ -440,15 +455,17 @@ __global__ void __launch_bounds__(kEgWarps * 32, 3)
 // The long segments' partial rows added in order: a warp per (segment, 32 E
 // columns) for those over few chunks, a CTA for the others, each of its warps a
 // contiguous share.
+constexpr int kEhWarps = 8;
+
 template <typename TT, int E, bool ACC>
-__global__ void __launch_bounds__(kEgWarps * 32)
+__global__ void __launch_bounds__(kEhWarps * 32)
     embed_grad_heavy_kernel(const uint2* __restrict__ list, const uint32_t* __restrict__ num_heavy,
                             const EmbedHeavy* __restrict__ heavy, uint32_t room, const float* __restrict__ part,
                             TT* __restrict__ dtable, uint32_t chunk, int64_t D, float scale) {
-  __shared__ float sh[kEgWarps][32 * E];
+  __shared__ float sh[kEhWarps][32 * E];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t tiles = static_cast<uint32_t>((D + 32 * E - 1) / (32 * E));
-  grid_dependency_wait();
+  grid_begin();
   const uint64_t few = static_cast<uint64_t>(num_heavy[0]) * tiles, many = static_cast<uint64_t>(num_heavy[1]) * tiles;
   // sum of partial rows a .. b - 1 of a segment that began in chunk `first`
   auto add_rows = [&](uint32_t first, uint32_t a, uint32_t b, int64_t k, float(&t)[E]) {
@@ -483,7 +500,7 @@ __global__ void __launch_bounds__(kEgWarps * 32)
   for (uint64_t it = blockIdx.x; it < many; it += gridDim.x) {
     const EmbedHeavy s = heavy[room - 1 - it / tiles];
     const int64_t k = static_cast<int64_t>(it % tiles) * (32 * E) + lane * E;
-    const uint32_t m = s.last - s.first + 1, per = (m + kEgWarps - 1) / kEgWarps;
+    const uint32_t m = s.last - s.first + 1, per = (m + kEhWarps - 1) / kEhWarps;
     add_rows(s.first, s.first + min(m, warp * per), s.first + min(m, (warp + 1) * per), k, t);
     __syncthreads();  // sh is still read from the item before
 #pragma unroll
@@ -494,14 +511,14 @@ __global__ void __launch_bounds__(kEgWarps * 32)
       for (int j = 0; j < E; ++j) {
         t[j] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kEgWarps; ++w) t[j] += sh[w][j * 32 + lane];
+        for (int w = 0; w < kEhWarps; ++w) t[j] += sh[w][j * 32 + lane];
       }
       write(s, k, t);
     }
   }
   // from the last CTA down: the first ones have the long segments
-  const uint64_t me = static_cast<uint64_t>(gridDim.x - 1 - blockIdx.x) * kEgWarps + warp;
-  for (uint64_t it = me; it < few; it += static_cast<uint64_t>(gridDim.x) * kEgWarps) {
+  const uint64_t me = static_cast<uint64_t>(gridDim.x - 1 - blockIdx.x) * kEhWarps + warp;
+  for (uint64_t it = me; it < few; it += static_cast<uint64_t>(gridDim.x) * kEhWarps) {
     const EmbedHeavy s = heavy[it / tiles];
     const int64_t k = static_cast<int64_t>(it % tiles) * (32 * E) + lane * E;
     add_rows(s.first, s.first, s.last + 1, k, t);

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kGcThreads)
     grad_norm_kernel(const __grid_constant__ GcParams<CAP> P, int chunks, double* __restrict__ sums) {
   __shared__ double sh[kGcThreads / 32];
   const int c0 = gc_begin(chunks, blockIdx.x, gridDim.x), c1 = gc_begin(chunks, blockIdx.x + 1, gridDim.x);
-  grid_dependents_launch();  // the next kernel may be scheduled; it waits for the sums
+  grid_begin();
   double s = 0.0;
   if (c0 < c1) {
     int i = P.first[blockIdx.x];
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kGcThreads)
     grad_scale_kernel(const __grid_constant__ GcParams<CAP> P, int chunks, const double* __restrict__ sums,
                       int num_sums, float max_norm, float* __restrict__ stats) {
   __shared__ double sh[kGcThreads / 32];
-  grid_dependency_wait();
+  grid_begin();
   double s = 0.0;
   for (int i = threadIdx.x; i < num_sums; i += kGcThreads) s += sums[i];
   const double norm = sqrt(gc_block_sum(s, sh));

@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(512)
   uint8_t* ring = smem + C::WB + group * (S * C::SLOT);
 #pragma unroll
   for (int i = 0; i < S; ++i) Row::template clear_pad<C::KP, T>(ring + i * C::SLOT, K, tid);
+  grid_begin();
   const TX* ahead = x + m * ldx;  // the row fetched next
   int64_t m_ahead = m;
   auto fetch = [&](int slot) {
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kNormThreads)
                       TY* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int64_t K,
                       float eps) {
   __shared__ float sh[3 * kNormWarps];
+  grid_begin();
   const int64_t m = blockIdx.x;
   const TX* xr = x + m * ldx;
   TY* yr = y + m * ldy;
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(256)
     }
     cp_async_commit();
   };
+  grid_dependency_wait();
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch(i, m + i * step);
   float c = 0.f, r = 0.f;
@@ -375,8 +378,8 @@ __global__ void __launch_bounds__(256)
     r = r_next;
     slot = slot + 1 == S ? 0 : slot + 1;
   }
-  if (!part) return;
   grid_dependents_launch();  // the kernel that adds the partial rows up may be scheduled; it waits for them
+  if (!part) return;  // the kernel that adds the partial rows up may be scheduled; it waits for them
   cp_async_wait<0>();
   __syncthreads();  // the ring is free: the warps' sums meet there
   float* acc = reinterpret_cast<float*>(smem);  // [warp][dweight | dbias][KP]
@@ -478,6 +481,7 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
       k[q] = m < M ? make_float2(mean[m], rstd[m]) : make_float2(0.f, 0.f);
     }
   };
+  grid_dependency_wait();
   fetch(0, tile);
   kept_of(tile, k_next);
 
@@ -614,8 +618,8 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
     }
     slot ^= 1;
   }
+  grid_dependents_launch();  // the kernel that adds the partial rows up may be scheduled; it waits for them
   if (!part) return;
-  grid_dependents_launch();
   float* pw = part + static_cast<int64_t>(blockIdx.x) * K;
   float* pb = pw + static_cast<int64_t>(gridDim.x) * K;
 #pragma unroll
@@ -642,6 +646,7 @@ __global__ void __launch_bounds__(kNormThreads)
                          const float* __restrict__ mean, const float* __restrict__ rstd, const TY* __restrict__ dy,
                          int64_t lddy, TX* __restrict__ dx, int64_t lddx, float* __restrict__ shift, int64_t K) {
   __shared__ float sh[3 * kNormWarps];
+  grid_begin();
   const int64_t m = blockIdx.x;
   const TX* xr = x + m * ldx;
   const TY* gr = dy + m * lddy;
@@ -679,6 +684,7 @@ __global__ void __launch_bounds__(kNormThreads)
                          const float* __restrict__ rstd, const float* __restrict__ shift, const TY* __restrict__ dy,
                          int64_t lddy, float* __restrict__ part, int64_t M, int64_t K) {
   __shared__ float sh[2][kNormWarps][32];
+  grid_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const int64_t p = blockIdx.y, P = gridDim.y;
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(kNormSumThreads)
                              float* __restrict__ db) {
   constexpr int WARPS = kNormSumThreads / 32;
   __shared__ float sh[WARPS][32];
-  grid_dependency_wait();
+  grid_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float* out = blockIdx.y == 0 ? dw : db;

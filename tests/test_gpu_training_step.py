@@ -92,3 +92,51 @@ def test_step_in_a_graph(bl):
         torch.cuda.synchronize()
         assert bl.device_error() == (0, 0)
         _check(s, r)
+
+
+def test_calls_after_other_work_in_a_graph(bl):
+    """Captured right behind copies, fills, a join of two streams and the library's other kernels: each call sees
+    what was written before it."""
+    g0 = torch.Generator().manual_seed(9)
+    src = torch.randn(300, 256, generator=g0).cuda()
+    w, b = torch.randn(256, generator=g0).cuda(), torch.randn(256, generator=g0).cuda()
+    ids_src = torch.randint(0, 40, (300,), generator=g0).cuda()
+    x, h, z = torch.empty_like(src), torch.empty_like(src), torch.empty(300, 256, dtype=BF16, device="cuda")
+    ids = torch.empty_like(ids_src)
+    W = (0.02 * torch.randn(384, 256, generator=g0)).cuda()
+
+    def step():
+        x.copy_(src)                                   # a copy
+        y, mean, rstd = bl.layer_norm(x, w, b, stats=True)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            h.copy_(y)
+            ids.copy_(ids_src)
+        z.zero_()
+        torch.cuda.current_stream().wait_stream(side)  # a join
+        dE = bl.embedding_backward(ids, h, 40)
+        e = bl.embedding(ids, dE)
+        dx, dw, db = bl.layer_norm_backward(x, w, mean, rstd, e)
+        packed, alpha = bl.bin_pack(W, bl.BL_PACK_FBI)
+        bl.layer_norm(dx, None, None, out=z)
+        # prefetches the packed weights before it waits
+        out = bl.bin_linear_w1a16(z[:8], packed, alpha, flags=bl.BL_FLAG_OVERLAP_PREVIOUS)
+        grads = [dE, dw, db]
+        norm, coef = bl.grad_clip(grads, 0.1)
+        return [y, e, dx, z, out, *grads, norm, coef]
+
+    step()
+    ref = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        for t in (x, h):
+            t.fill_(7.0)
+        ids.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(ref, got))
+    assert bl.device_error() == (0, 0)
