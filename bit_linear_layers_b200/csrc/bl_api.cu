@@ -620,12 +620,14 @@ int with_norm_tile(int64_t K, bool wide, bool few, F&& f) {
     if (K <= 1024) return f(Int<8>{}, Int<4>{});
     if (K <= 2048) return f(Int<16>{}, Int<4>{});
     if (K <= 4096) return f(Int<16>{}, Int<8>{});
+    if (K <= 5120) return f(Int<16>{}, Int<10>{});
     return f(Int<16>{}, Int<16>{});
   }
   if (K <= 512) return f(Int<16>{}, Int<1>{});
   if (K <= 1024) return f(Int<32>{}, Int<1>{});
   if (K <= 2048) return f(Int<32>{}, Int<2>{});
   if (K <= 4096) return f(Int<32>{}, Int<4>{});
+  if (K <= 6144) return f(Int<32>{}, Int<6>{});
   return f(Int<32>{}, Int<8>{});
 }
 
@@ -1393,53 +1395,68 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     double* sums = static_cast<double*>(ws);
     const int ctas = std::min(sms * 8, kGcMaxCtas);
-    // launches of up to kGcMaxTensors tensors: all the norms, then all the products
-    int num_sums = 0;
-    auto pass = [&](auto cap, bool norms) {
+    // launches of up to CAP tensors: all the norms, then all the products
+    auto run = [&](auto cap) {
       constexpr int CAP = decltype(cap)::value;
       static thread_local GcParams<CAP> P;
-      int i = 0, launch = 0;
-      do {
+      int chunks = 0, grid = 1;
+      bool writes = false;
+      // the tensors of a launch that begins at tensor i; returns where the next one begins
+      auto fill = [&](int i) {
         int n = 0;
-        int64_t chunks = 0;
-        bool writes = false;
+        int64_t total_chunks = 0;
+        writes = false;
         for (; i < num_tensors && n < CAP; ++i) {
           const bl_grad_tensor& t = tensors[i];
           if (t.numel == 0) continue;
           const int es = type_bytes(t.type);
           P.t[n] = GcTensor{t.g, t.out, t.numel};
           P.f32[n] = t.type == BL_TYPE_F32;
-          P.chunk0[n] = static_cast<int32_t>(chunks);
+          P.chunk0[n] = static_cast<int32_t>(total_chunks);
           const int64_t mis = int64_t(reinterpret_cast<uintptr_t>(t.g) & 15u) / es;
-          chunks += cdiv(t.numel + mis, int64_t(kGcChunkVecs) * 16 / es);
+          total_chunks += cdiv(t.numel + mis, int64_t(kGcChunkVecs) * 16 / es);
           writes |= t.out != nullptr;
           ++n;
         }
-        P.chunk0[n] = static_cast<int32_t>(chunks);
-        const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, ctas)));
-        for (int b = 0, at = 0; b <= grid; ++b) {
-          const int c = std::min(gc_begin(int(chunks), b, grid), std::max(0, int(chunks) - 1));
+        P.chunk0[n] = static_cast<int32_t>(total_chunks);
+        chunks = static_cast<int>(total_chunks);
+        grid = std::max(1, std::min(chunks, ctas));
+        const int q = chunks / grid, r = chunks % grid;
+        for (int b = 0, c = 0, at = 0; b <= grid; ++b) {
           while (at + 1 < n && P.chunk0[at + 1] <= c) ++at;
           P.first[b] = static_cast<uint16_t>(at);
+          c = std::min(c + q + (b < r ? 1 : 0), std::max(0, chunks - 1));
         }
-        int st = BL_OK;
-        if (norms) {
-          st = launch_after(grad_norm_kernel<CAP>, dim3(unsigned(grid)), kGcThreads, 0, s, P, int(chunks), sums + num_sums);
-          num_sums += grid;
-        } else if (writes || launch == 0) {
-          st = launch_after(grad_scale_kernel<CAP>, dim3(writes ? unsigned(grid) : 1u), kGcThreads, 0, s, P, writes ? int(chunks) : 0,
-                            static_cast<const double*>(sums), num_sums, max_norm, launch == 0 ? stats : nullptr);
-        }
-        ++launch;
-        if (st != BL_OK) return st;
-      } while (i < num_tensors);
-      return int(BL_OK);
+        return i;
+      };
+      int num_sums = 0;
+      auto norm = [&] {
+        const int st = launch_after(grad_norm_kernel<CAP>, dim3(unsigned(grid)), kGcThreads, 0, s, P, chunks, sums + num_sums);
+        num_sums += grid;
+        return st;
+      };
+      auto scale = [&](bool first) {
+        if (!writes && !first) return int(BL_OK);
+        return launch_after(grad_scale_kernel<CAP>, dim3(writes ? unsigned(grid) : 1u), kGcThreads, 0, s, P,
+                            writes ? chunks : 0, static_cast<const double*>(sums), num_sums, max_norm,
+                            first ? stats : nullptr);
+      };
+      int end = fill(0);
+      int st = norm();
+      if (end == num_tensors) return st != BL_OK ? st : scale(true);  // one launch: the table is still there
+      while (st == BL_OK && end < num_tensors) {
+        end = fill(end);
+        st = norm();
+      }
+      end = 0;
+      for (bool first = true; st == BL_OK && end < num_tensors; first = false) {
+        end = fill(end);
+        st = scale(first);
+      }
+      return st;
     };
     // descriptors are copied with each launch: no more of them than there are
-    auto run = [&](auto cap) {
-      const int st = pass(cap, true);
-      return st != BL_OK ? st : pass(cap, false);
-    };
+    // descriptors are copied with each launch: no more of them than there are
     if (num_tensors <= 32) return run(Int<32>{});
     return num_tensors <= 256 ? run(Int<256>{}) : run(Int<kGcMaxTensors>{});
   } catch (...) {  // out of host memory

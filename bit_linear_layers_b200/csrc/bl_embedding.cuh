@@ -135,7 +135,7 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
     const int shift = pass * digit_bits;
     const uint2* in = p.list[(pass + 1) & 1];
     uint2* out = p.list[pass & 1];
-    uint32_t kh[kEsHold], vh[kEsHold], same[kEsHold];
+    uint32_t kh[kEsHold], vh[kEsHold];
     // the block of positions b0 + 32 u + lane (key V + 1: none)
     auto load = [&](uint32_t b0) {
 #pragma unroll
@@ -148,29 +148,14 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
           vh[u] = kv.y;
         }
       }
-      // lanes with the same digit, one vote per bit (atomics on a frequent token's count take turns, up to 32
-      // of them)
-#pragma unroll
-      for (int u = 0; u < kEsHold; ++u) {
-        if (b0 + 32 * u >= w1) break;  // uniform over the warp
-        same[u] = __ballot_sync(0xffffffffu, kh[u] <= V);
-        for (int b = 0; b < digit_bits; ++b) {
-          const bool bit = (kh[u] >> (shift + b)) & 1u;
-          const uint32_t votes = __ballot_sync(0xffffffffu, bit);
-          same[u] &= bit ? votes : ~votes;
-        }
-      }
     };
     for (int d = lane; d < kEsBins; d += 32) hist[warp][d] = 0u;
     __syncwarp();
     for (uint32_t b0 = w0; b0 < w1; b0 += kEsHold * 32) {
       load(b0);
 #pragma unroll
-      for (int u = 0; u < kEsHold; ++u) {
-        if (b0 + 32 * u >= w1) break;
-        if (kh[u] <= V && (same[u] & ((1u << lane) - 1u)) == 0u) hist[warp][(kh[u] >> shift) & mask] += __popc(same[u]);
-        __syncwarp();
-      }
+      for (int u = 0; u < kEsHold; ++u)
+        if (kh[u] <= V) atomicAdd(&hist[warp][(kh[u] >> shift) & mask], 1u);
     }
     __syncthreads();
     // digit d: counts of the warps ahead, this CTA's total
@@ -233,11 +218,18 @@ __device__ __forceinline__ void embed_sort(uint32_t (*hist)[kEsBins], const TI* 
           const int64_t id = static_cast<int64_t>(ids[vh[u]]);
           if (id < 0 || id >= V) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingGradId);
         }
-        const uint32_t before = __popc(same[u] & ((1u << lane) - 1u));
+        // lanes with the same digit, one vote per bit
+        uint32_t same = __ballot_sync(0xffffffffu, live);
+        for (int b = 0; b < digit_bits; ++b) {
+          const bool bit = (dig >> b) & 1u;
+          const uint32_t votes = __ballot_sync(0xffffffffu, bit);
+          same &= bit ? votes : ~votes;
+        }
+        const uint32_t before = __popc(same & ((1u << lane) - 1u));
         uint32_t at = 0;
         if (live) at = hist[warp][dig] + before;
         __syncwarp();
-        if (live && before == 0) hist[warp][dig] += __popc(same[u]);
+        if (live && before == 0) hist[warp][dig] += __popc(same);
         __syncwarp();
         if (live) out[at] = make_uint2(kh[u], vh[u]);
       }

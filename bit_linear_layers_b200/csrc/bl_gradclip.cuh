@@ -27,7 +27,7 @@ struct GcTensor {
   void* out;
   int64_t numel;
 };
-// CTA b takes chunks [n b / grid, n (b + 1) / grid). Parameters are read through
+// CTA b takes the chunks from gc_begin(b) to gc_begin(b + 1). Parameters are read through
 // the constant cache, a miss at a time: the tensor of a CTA's first chunk is
 // looked up by the host (a search over the table took longer than the sums of a
 // small model).
@@ -35,12 +35,14 @@ template <int CAP>
 struct GcParams {
   GcTensor t[CAP];
   int32_t chunk0[CAP + 1];     // first chunk of each tensor
-  uint16_t first[kGcMaxCtas + 1];  // tensor of chunk n b / grid
+  uint16_t first[kGcMaxCtas + 1];  // tensor of CTA b's first chunk; [grid]: of the last chunk
   uint8_t f32[CAP];
 };
 
+// first chunk of CTA b: the first chunks % grid CTAs have one more than the others
 __host__ __device__ inline int gc_begin(int chunks, int b, int grid) {
-  return static_cast<int>(static_cast<int64_t>(chunks) * b / grid);
+  const int q = chunks / grid, r = chunks - q * grid;
+  return b * q + (b < r ? b : r);
 }
 
 template <typename T>
