@@ -10,10 +10,11 @@ nvcc cross-compiles, so this runs on machines without a GPU.
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "bl_api.cu")
+SRCS = [os.path.join(PKG, "csrc", f) for f in ("bl_api.cu", "bl_norm.cu")]
 LIB = os.path.join(PKG, "libbitlinear.so")
 BINDING_SRC = os.path.join(PKG, "csrc", "bl_binding.cpp")
 BINDING = os.path.join(PKG, "_native.so")
@@ -22,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC,-Wall", "-shared",
+    "-Xcompiler", "-fPIC,-Wall",
     "--expt-relaxed-constexpr",
 ]
 
@@ -34,10 +35,14 @@ def sources():
 
 def build(verbose_ptxas: bool = False, out: str = LIB) -> str:
     nvcc = os.environ.get("NVCC", "nvcc")
-    cmd = [nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-o", out, SRC]
-    if verbose_ptxas:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+    flags = (["-Xptxas=-v"] if verbose_ptxas else []) + NVCC_FLAGS
+    with tempfile.TemporaryDirectory() as tmp:  # the translation units side by side
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in SRCS]
+        running = [subprocess.Popen([nvcc, *flags, "-I", INCLUDE, "-c", "-o", o, s]) for s, o in zip(SRCS, objs)]
+        failed = [s for s, p in zip(SRCS, running) if p.wait() != 0]
+        if failed:
+            raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
+        subprocess.run([nvcc, *NVCC_FLAGS, "-shared", "-o", out, *objs], check=True)
     if out == LIB:
         build_binding()
     return out

@@ -1,13 +1,13 @@
 // libbitlinear.so: the C ABI declared in include/bitlinear.h.
 //
 // Host side only: argument validation, per-device one-time set-up, TMA
-// descriptor encoding and kernel dispatch. All kernels live in the headers
-// included below, so the library is one translation unit (no relocatable
-// device code). Nothing here allocates memory.
+// descriptor encoding and kernel dispatch. The kernels live in the headers
+// included below; the layer norms have a translation unit of their own
+// (bl_norm.cu; no relocatable device code, nothing on the device is shared
+// between the two). Nothing here allocates memory.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 #include <cmath>
 #include <cstring>
@@ -28,21 +28,13 @@
 #include "bl_gemv_stream_mma.cuh"
 #include "bl_gemv_w1a8_mma.cuh"
 #include "bl_gradclip.cuh"
-#include "bl_layernorm.cuh"
+#include "bl_host.cuh"
 #include "bl_lnquant.cuh"
 #include "bl_pack.cuh"
 #include "bl_xnor.cuh"
 
 namespace bl {
 namespace {
-
-constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxProduct = int64_t(1) << 40;
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-
-inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---- per-device set-up ------------------------------------------------------
 struct DeviceState {
@@ -59,11 +51,6 @@ struct DeviceState {
   int stack_mma_clusters[2] = {0, 0};
 };
 DeviceState g_devices[kMaxDevices];
-
-template <typename Kernel>
-bool set_smem(Kernel k, int bytes) {
-  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
 
 // every tensor-core GEMM configuration the dispatch below can launch
 template <int KIND, int T>
@@ -182,11 +169,6 @@ int cluster_capacity(int S) {
     return 0;
   }
   return g_devices[dev].cluster_cap[S];
-}
-
-int launch_status() {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? BL_OK : BL_ERR_CUDA;
 }
 
 // ---- TMA descriptors ----------------------------------------------------------
@@ -534,37 +516,6 @@ int w1a8_impl(const uint16_t* x, const uint32_t* packed, const float* beta, floa
 }
 
 // ---- full-precision operators of a training step --------------------------------
-constexpr int64_t kMaxIds = (int64_t(1) << 31) - 1;
-
-inline bool type_ok(int type) { return type == BL_TYPE_BF16 || type == BL_TYPE_F32; }
-inline int type_bytes(int type) { return type == BL_TYPE_F32 ? 4 : 2; }
-inline bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes) == 0; }
-
-// rows of K elements with a pitch of ld elements, all below 2^40 elements
-int check_rows(int64_t M, int64_t K, int64_t ld) {
-  if (ld < K) return BL_ERR_INVALID_ARG;
-  if (ld > kMaxProduct || (M > 0 && ld >= kMaxProduct / M)) return BL_ERR_UNSUPPORTED;
-  return BL_OK;
-}
-int check_norm_shape(int64_t M, int64_t K) {
-  if (M < 0 || K < 1) return BL_ERR_INVALID_ARG;
-  return M > kMaxDim || K > kMaxDim ? BL_ERR_UNSUPPORTED : BL_OK;
-}
-
-struct NormWs {
-  int64_t parts;  // partial rows of dweight and of dbias there is room for
-  size_t shift, part, bytes;
-};
-NormWs norm_ws(int64_t M, int64_t K) {
-  NormWs w{};
-  if (M < 1 || K < 1 || M > kMaxDim || K > kMaxDim || M >= kMaxProduct / K) return w;
-  w.parts = std::min<int64_t>(M, K <= 1024 ? kNormMaxParts : kNormMaxParts / 2);
-  w.shift = 0;
-  w.part = align256(size_t(M) * 4);
-  w.bytes = w.part + align256(size_t(2 * w.parts) * size_t(K) * 4);
-  return w;
-}
-
 struct EmbedWs {
   int64_t chunk, chunks;  // sorted positions per warp of the sums
   size_t list[2], num_heavy, heavy, part, bytes;
@@ -596,98 +547,10 @@ inline bool rows_vec(const void* p, int type, int64_t ld, int64_t K, int64_t M) 
   return K % 8 == 0 && (M <= 1 || ld % 8 == 0) && aligned_to(p, 8 * type_bytes(type));
 }
 
-template <int V>
-using Int = std::integral_constant<int, V>;
-
-// rows that `elems` elements at a time can be read or written of
-inline bool rows_aligned(const void* p, int type, int64_t ld, int64_t K, int64_t M, int elems) {
-  return K % elems == 0 && (M <= 1 || ld % elems == 0) && aligned_to(p, elems * type_bytes(type));
-}
-// rows whose 16-byte pieces can be copied whole
-inline bool rows_in_pieces(const void* p, int type, int64_t ld, int64_t K, int64_t M) {
-  return rows_aligned(p, type, ld, K, M, 16 / type_bytes(type));
-}
-
-// The layer norm's tiling: f(CPT, W) (columns per thread, warps per row) of the
-// smallest tile that holds a row. 32 columns per thread where they are read many
-// at a time, fewer where they are read one by one (`wide` false) or where the
-// rows are so few (`few`) that spreading each over a CTA is what fills the GPU.
-template <typename F>
-int with_norm_tile(int64_t K, bool wide, bool few, F&& f) {
-  if (K <= 256 && !few) return f(Int<8>{}, Int<1>{});
-  if (K > 8192) return f(Int<32>{}, Int<16>{});
-  if (few || !wide) {
-    if (K <= 1024) return f(Int<8>{}, Int<4>{});
-    if (K <= 2048) return f(Int<16>{}, Int<4>{});
-    if (K <= 4096) return f(Int<16>{}, Int<8>{});
-    if (K <= 5120) return f(Int<16>{}, Int<10>{});
-    return f(Int<16>{}, Int<16>{});
-  }
-  if (K <= 512) return f(Int<16>{}, Int<1>{});
-  if (K <= 1024) return f(Int<32>{}, Int<1>{});
-  if (K <= 2048) return f(Int<32>{}, Int<2>{});
-  if (K <= 4096) return f(Int<32>{}, Int<4>{});
-  if (K <= 6144) return f(Int<32>{}, Int<6>{});
-  return f(Int<32>{}, Int<8>{});
-}
-
-// CTAs per SM of a kernel on the current device, looked up once per device
-// (and its dynamic shared memory allowed)
-template <auto Kernel>
-int ctas_per_sm(int threads, int smem) {
-  static std::atomic<int> known[kMaxDevices];
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return 0;
-  }
-  int n = known[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if ((smem > 0 && !set_smem(Kernel, smem)) ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, size_t(smem)) != cudaSuccess) {
-      cudaGetLastError();
-      return 0;
-    }
-    known[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-// CTAs of a persistent kernel over `units`: as many as fit at once, evenly loaded
-inline int64_t persistent_grid(int ctas_per_sm, int sms, int64_t units, int64_t most) {
-  const int64_t cap = std::min<int64_t>(int64_t(ctas_per_sm) * sms, most);
-  return units <= cap ? units : cdiv(units, cdiv(units, cap));
-}
-
-// launch with programmatic serialisation: the kernel may be scheduled while
-// the one before it runs, and waits for it by itself
-template <typename... Params, typename... Args>
-int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return BL_ERR_CUDA;
-  }
-  return launch_status();
-}
-
-// f(uint16_t or float of `a`, of `b`)
-template <typename F>
-int with_types(int a, int b, F&& f) {
-  if (a == BL_TYPE_F32) return b == BL_TYPE_F32 ? f(float{}, float{}) : f(float{}, uint16_t{});
-  return b == BL_TYPE_F32 ? f(uint16_t{}, float{}) : f(uint16_t{}, uint16_t{});
-}
-
 }  // namespace
+
+int library_device(int* num_sms) { return device_setup(num_sms); }
+
 }  // namespace bl
 
 using namespace bl;
@@ -728,7 +591,7 @@ size_t bl_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {
              align256(size_t(K) * 4) + align256(size_t(K) * Mp * 2) + align256(size_t(N) * Mp * 2) +
              align256(size_t(K / kSsRowsA) * size_t(N) * 4);
     }
-    case BL_OP_LAYER_NORM_BACKWARD: return norm_ws(M, K).bytes;
+    case BL_OP_LAYER_NORM_BACKWARD: return norm_workspace_bytes(M, K);
     case BL_OP_EMBEDDING_BACKWARD: return embed_ws(M, N, K).bytes;
     case BL_OP_GRAD_CLIP: return size_t(gc_launches(M)) * kGcMaxCtas * sizeof(double);
     default: return 0;
@@ -1112,136 +975,6 @@ int bin_xnor_gemm(const uint32_t* a, const uint32_t* b, int32_t* dot, int64_t M,
   return launch_status();
 }
 
-int bl_layer_norm(const void* x, int x_type, int64_t ldx, const float* weight, const float* bias, void* y, int y_type,
-                  int64_t ldy, float* mean, float* rstd, int64_t M, int64_t K, float eps, void* stream) {
-  int rc = check_norm_shape(M, K);
-  if (rc != BL_OK) return rc;
-  if (!type_ok(x_type) || !type_ok(y_type) || !(eps > 0.f) || !(eps < INFINITY)) return BL_ERR_INVALID_ARG;
-  if ((rc = check_rows(M, K, ldx)) != BL_OK || (rc = check_rows(M, K, ldy)) != BL_OK) return rc;
-  if (M == 0) return BL_OK;
-  if (!x || !y || !aligned_to(x, type_bytes(x_type)) || !aligned_to(y, type_bytes(y_type)) || !aligned_to(weight, 4) ||
-      !aligned_to(bias, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
-    return BL_ERR_INVALID_ARG;
-  if (x == y && (x_type != y_type || ldx != ldy)) return BL_ERR_INVALID_ARG;
-  int sms = 0;
-  rc = device_setup(&sms);
-  if (rc != BL_OK) return rc;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return with_types(x_type, y_type, [&](auto tx, auto ty) {
-    using TX = decltype(tx);
-    using TY = decltype(ty);
-    if (K > kNormMaxK) {
-      return launch_after(layer_norm_kernel<TX, TY>, dim3(unsigned(M)), kNormThreads, 0, s, static_cast<const TX*>(x), ldx,
-                          weight, bias, static_cast<TY*>(y), ldy, mean, rstd, K, eps);
-    }
-    constexpr int WIDE = 16 / int(sizeof(TX));
-    const bool wide = rows_aligned(x, x_type, ldx, K, M, WIDE) && rows_aligned(y, y_type, ldy, K, M, WIDE);
-    return with_norm_tile(K, wide, M <= 2 * int64_t(sms), [&](auto cpt, auto warps) {
-      auto run = [&](auto e) {
-        constexpr int E = decltype(e)::value, CPT = decltype(cpt)::value, W = decltype(warps)::value;
-        using C = NormCfg<TX, E, CPT, W>;
-        constexpr auto kernel = layer_norm_rows_kernel<TX, TY, E, CPT, W>;
-        const int groups = int(std::min<int64_t>(C::GROUPS, cdiv(M, sms)));
-        // with fewer groups more CTAs fit, but then there are no rows for them
-        const int n = ctas_per_sm<kernel>(C::GROUPS * W * 32, C::smem(C::GROUPS));
-        if (n < 1) return int(BL_ERR_CUDA);
-        const int64_t grid = persistent_grid(n, sms, cdiv(M, groups), kMaxDim);
-        return launch_after(kernel, dim3(unsigned(grid)), groups * W * 32, C::smem(groups), s, static_cast<const TX*>(x),
-                            ldx, weight, bias, static_cast<TY*>(y), ldy, mean, rstd, M, int(K), eps);
-      };
-      return wide ? run(Int<WIDE>{}) : run(Int<1>{});
-    });
-  });
-}
-
-int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* weight, const float* mean,
-                           const float* rstd, const void* dy, int dy_type, int64_t lddy, void* dx, int64_t lddx,
-                           float* dweight, float* dbias, int64_t M, int64_t K, void* ws, size_t ws_bytes, void* stream) {
-  int rc = check_norm_shape(M, K);
-  if (rc != BL_OK) return rc;
-  if (!type_ok(x_type) || !type_ok(dy_type)) return BL_ERR_INVALID_ARG;
-  if ((rc = check_rows(M, K, ldx)) != BL_OK || (rc = check_rows(M, K, lddy)) != BL_OK ||
-      (dx && (rc = check_rows(M, K, lddx)) != BL_OK))
-    return rc;
-  if (!aligned_to(weight, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4)) return BL_ERR_INVALID_ARG;
-  if (dweight && dweight == dbias) return BL_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M == 0) {  // an empty batch: zero gradients of the weight and the bias
-    for (float* g : {dweight, dbias})
-      if (g && cudaMemsetAsync(g, 0, size_t(K) * 4, s) != cudaSuccess) {
-        cudaGetLastError();
-        return BL_ERR_CUDA;
-      }
-    return BL_OK;
-  }
-  if (!x || !mean || !rstd || !dy || !aligned_to(x, type_bytes(x_type)) || !aligned_to(dy, type_bytes(dy_type)) ||
-      !aligned_to(dx, type_bytes(x_type)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || dx == x ||
-      (dx && dx == dy))
-    return BL_ERR_INVALID_ARG;
-  const bool want_dw = dweight || dbias;
-  if (!dx && !want_dw) return BL_OK;
-  const NormWs w = norm_ws(M, K);
-  if (w.bytes == 0) return BL_ERR_UNSUPPORTED;
-  if (want_dw && (!ws || !aligned16(ws) || ws_bytes < w.bytes)) return BL_ERR_INVALID_ARG;
-  int sms = 0;
-  rc = device_setup(&sms);
-  if (rc != BL_OK) return rc;
-  float* shift = want_dw ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.shift) : nullptr;
-  float* part = want_dw ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part) : nullptr;
-  return with_types(x_type, dy_type, [&](auto tx, auto ty) {
-    using TX = decltype(tx);
-    using TY = decltype(ty);
-    const auto* xp = static_cast<const TX*>(x);
-    const auto* gp = static_cast<const TY*>(dy);
-    auto* dxp = static_cast<TX*>(dx);
-    auto sum_parts = [&](int64_t parts) {
-      return launch_after(layer_norm_dw_sum_kernel, dim3(unsigned(cdiv(K, 32)), 2), kNormSumThreads, 0, s,
-                          static_cast<const float*>(part), int(parts), K, dweight, dbias);
-    };
-    if (K > kNormGradMaxK) {
-      int st = launch_after(layer_norm_dx_kernel<TX, TY>, dim3(unsigned(M)), kNormThreads, 0, s, xp, ldx, weight, mean,
-                            rstd, gp, lddy, dxp, lddx, shift, K);
-      if (st != BL_OK || !want_dw) return st;
-      const int64_t parts = std::min<int64_t>(cdiv(M, 64), 128);
-      st = launch_after(layer_norm_dw_kernel<TX, TY>, dim3(unsigned(cdiv(K, 32)), unsigned(parts)), kNormThreads, 0, s, xp,
-                        ldx, mean, rstd, static_cast<const float*>(shift), gp, lddy, part, M, K);
-      return st != BL_OK ? st : sum_parts(parts);
-    }
-    auto launch = [&](auto kernel, int ctas, int threads, int smem, int64_t units) {
-      if (ctas < 1) return int(BL_ERR_CUDA);
-      const int64_t grid = persistent_grid(ctas, sms, units, want_dw ? w.parts : units);
-      const int st = launch_after(kernel, dim3(unsigned(grid)), threads, smem, s, xp, ldx, weight, mean, rstd, gp, lddy,
-                                  dxp, lddx, part, M, int(K));
-      return st != BL_OK || !want_dw ? st : sum_parts(grid);
-    };
-    constexpr int WIDE = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
-    const bool wide = rows_in_pieces(x, x_type, ldx, K, M) && rows_in_pieces(dy, dy_type, lddy, K, M) &&
-                      (!dx || rows_in_pieces(dx, x_type, lddx, K, M));
-    auto by_width = [&](auto e) {
-      constexpr int E = decltype(e)::value;
-      auto rows = [&](auto cpt) {
-        constexpr int CPT = decltype(cpt)::value;
-        using C = NormGradRowCfg<TX, TY, E, CPT>;
-        constexpr auto kernel = layer_norm_grad_rows_kernel<TX, TY, E, CPT>;
-        return launch(kernel, ctas_per_sm<kernel>(C::WARPS * 32, C::SMEM), C::WARPS * 32, C::SMEM, cdiv(M, C::WARPS));
-      };
-      auto tiles = [&](auto cpt, auto warps) {
-        constexpr int CPT = decltype(cpt)::value, W = decltype(warps)::value;
-        using C = NormGradTileCfg<TX, TY, E, CPT, W>;
-        constexpr auto kernel = layer_norm_grad_tile_kernel<TX, TY, E, CPT, W>;
-        return launch(kernel, ctas_per_sm<kernel>(C::THREADS, C::SMEM), C::THREADS, C::SMEM, cdiv(M, C::R));
-      };
-      if (K <= 256) return rows(Int<8>{});
-      if (K <= 512) return rows(Int<16>{});
-      if (K <= 1024) return tiles(Int<8>{}, Int<4>{});
-      if (K <= 2048) return tiles(Int<8>{}, Int<8>{});
-      if (K <= 4096) return tiles(Int<8>{}, Int<16>{});
-      return tiles(Int<32>{}, Int<8>{});
-    };
-    return wide ? by_width(Int<WIDE>{}) : by_width(Int<1>{});
-  });
-}
-
 int bl_embedding(const void* ids, int id_type, const void* table, int table_type, void* y, int y_type, int64_t T,
                  int64_t V, int64_t D, float scale, void* stream) {
   if (T < 0 || V < 1 || D < 1) return BL_ERR_INVALID_ARG;
@@ -1379,7 +1112,8 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
       const uintptr_t o = reinterpret_cast<uintptr_t>(t.out);
       if (t.out) outs.push_back(Range{o, o + uintptr_t(t.numel) * uintptr_t(es), i});
     }
-    std::sort(outs.begin(), outs.end(), [](const Range& l, const Range& r) { return l.a < r.a; });
+    const auto before = [](const Range& l, const Range& r) { return l.a < r.a; };
+    if (!std::is_sorted(outs.begin(), outs.end(), before)) std::sort(outs.begin(), outs.end(), before);
     for (size_t j = 1; j < outs.size(); ++j)
       if (outs[j].a < outs[j - 1].b) return BL_ERR_INVALID_ARG;
     for (int i = 0; i < num_tensors && !outs.empty(); ++i) {

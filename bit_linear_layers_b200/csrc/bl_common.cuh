@@ -15,14 +15,14 @@
 namespace bl {
 
 // ---------------------------------------------------------------------------
-// In-kernel fault record. One per device (this library is a single
-// translation unit). A kernel that gives up on a bounded wait records the
+// In-kernel fault record. One per device, in bl_api.cu's translation unit: the
+// kernels that record faults are all built there. A kernel that gives up on a bounded wait records the
 // first failure here and returns; the host reads it with bl_device_error.
 struct DeviceError {
   int code;   // 0 or a BL_ERR_* value
   int where;  // which kernel / wait gave up (kWhere* below)
 };
-__device__ DeviceError g_device_error;
+static __device__ DeviceError g_device_error;
 
 enum : int {
   kWhereGemmProducer = 1,

@@ -57,7 +57,7 @@ __device__ __forceinline__ int wb_at(int k, int kp) {
 }
 
 template <typename TX, typename TY, int E, int CPT, int W>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__((NormCfg<TX, E, CPT, W>::GROUPS * W * 32))
     layer_norm_rows_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w,
                            const float* __restrict__ b, TY* __restrict__ y, int64_t ldy, float* __restrict__ mean,
                            float* __restrict__ rstd, int64_t M, int K, float eps) {
