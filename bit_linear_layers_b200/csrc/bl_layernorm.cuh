@@ -418,7 +418,9 @@ struct NormGradTileCfg {
   static constexpr int KP = CPT * W * 32, THREADS = W * 32;
   static constexpr int SLOT_X = KP * int(sizeof(TX)) + StagedRow<TX, E>::PAD;
   static constexpr int SLOT = SLOT_X + KP * int(sizeof(TG)) + StagedRow<TG, E>::PAD;
-  static constexpr int CTAS = W <= 4 ? 3 : 1, LIMIT = 222 * 1024 / CTAS - KP * 4;
+  // rows of any alignment take more instructions per element: more warps, smaller tiles
+  static constexpr int CTAS = E == 1 ? (W <= 4 ? 5 : W <= 10 && CPT == 8 ? 2 : 1) : W <= 4 ? 3 : 1;
+  static constexpr int LIMIT = 222 * 1024 / CTAS - KP * 4;
   static constexpr int R = 2 * 8 * SLOT <= LIMIT ? 8 : 2 * 4 * SLOT <= LIMIT ? 4 : 2 * 2 * SLOT <= LIMIT ? 2 : 1;
   static constexpr int TILE = R * SLOT;
   static constexpr int SMEM = 2 * TILE + KP * 4;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
     layer_norm_grad_tile_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w,
                                 const float* __restrict__ mean, const float* __restrict__ rstd,
                                 const TG* __restrict__ dy, int64_t lddy, TX* __restrict__ dx, int64_t lddx,
-                                float* __restrict__ part, int64_t M, int K) {
+                                float* __restrict__ part, int64_t M, int K, int height) {
   using C = NormGradTileCfg<TX, TG, E, CPT, W>;
   using RowX = StagedRow<TX, E>;
   using RowG = StagedRow<TG, E>;
@@ -443,8 +445,9 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
   __shared__ float4 consts[R];         // -c, r, -md r, -r mean g
   __shared__ float consts1[R];         // -r mean(g z)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int my_row = P > 1 ? warp / P : warp * Q, my_part = P > 1 ? warp % P : 0;
-  const int64_t tiles = (M + R - 1) / R;
+  // this warp's rows of a tile: my_row + q * W
+  const int my_row = P > 1 ? warp / P : warp, my_part = P > 1 ? warp % P : 0;
+  const int64_t tiles = (M + height - 1) / height;  // of `height` <= R rows
   float* wplane = reinterpret_cast<float*>(smem);  // the weight, in planes of four columns
   uint8_t* ring = smem + C::KP * 4;
 
@@ -456,9 +459,9 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
     RowG::template clear_pad<C::KP, T>(ring + i * C::SLOT + C::SLOT_X, K, tid);
   }
   auto fetch = [&](int slot, int64_t t) {
-    const int rows = t >= tiles ? 0 : static_cast<int>(M - t * R < R ? M - t * R : R);
-    const TX* xt = x + t * R * ldx;
-    const TG* gt = dy + t * R * lddy;
+    const int rows = t >= tiles ? 0 : static_cast<int>(M - t * height < height ? M - t * height : height);
+    const TX* xt = x + t * height * ldx;
+    const TG* gt = dy + t * height * lddy;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (i < rows) {
@@ -477,8 +480,9 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
   auto kept_of = [&](int64_t t, float2(&k)[Q]) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int64_t m = t * R + my_row + q;
-      k[q] = m < M ? make_float2(mean[m], rstd[m]) : make_float2(0.f, 0.f);
+      const int row = my_row + q * W;
+      const int64_t m = t * height + row;
+      k[q] = row < height && m < M ? make_float2(mean[m], rstd[m]) : make_float2(0.f, 0.f);
     }
   };
   grid_dependency_wait();
@@ -521,9 +525,9 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
 
   int slot = 0;
   for (; tile < tiles; tile += step) {
-    const int rows = static_cast<int>(M - tile * R < R ? M - tile * R : R);
-    const TX* xt = x + tile * R * ldx;
-    const TG* gt = dy + tile * R * lddy;
+    const int rows = static_cast<int>(M - tile * height < height ? M - tile * height : height);
+    const TX* xt = x + tile * height * ldx;
+    const TG* gt = dy + tile * height * lddy;
     cp_async_wait<0>();
     __syncthreads();  // the tile has arrived; the other slot and the constants are free
     fetch(slot ^ 1, tile + step);
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
 
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int row = my_row + q;
+      const int row = my_row + q * W;
       if (row < rows) {
         const uint8_t* at = ring + slot * C::TILE + row * C::SLOT;
         const uint8_t *xs = RowX::first(at, xt + row * ldx), *gs = RowG::first(at + C::SLOT_X, gt + row * lddy);
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
       }
       __syncthreads();
     }
-    TX* dxt = dx + (dx ? tile * R * lddx : 0);
+    TX* dxt = dx + (dx ? tile * height * lddx : 0);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (i >= rows) break;

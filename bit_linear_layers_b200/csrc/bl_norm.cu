@@ -178,13 +178,12 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
                         ldx, mean, rstd, static_cast<const float*>(shift), gp, lddy, part, M, K);
       return st != BL_OK ? st : sum_parts(parts);
     }
-    auto launch = [&](auto kernel, int ctas, int threads, int smem, int64_t units) {
-      if (ctas < 1) return int(BL_ERR_CUDA);
-      const int64_t grid = persistent_grid(ctas, sms, units, want_dw ? w.parts : units);
+    auto launch = [&](auto kernel, int64_t grid, int threads, int smem, auto... more) {
       const int st = launch_after(kernel, dim3(unsigned(grid)), threads, smem, s, xp, ldx, weight, mean, rstd, gp, lddy,
-                                  dxp, lddx, part, M, int(K));
+                                  dxp, lddx, part, M, int(K), more...);
       return st != BL_OK || !want_dw ? st : sum_parts(grid);
     };
+    const int64_t most = want_dw ? w.parts : kMaxDim;
     constexpr int WIDE = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
     const bool wide = rows_in_pieces(x, x_type, ldx, K, M) && rows_in_pieces(dy, dy_type, lddy, K, M) &&
                       (!dx || rows_in_pieces(dx, x_type, lddx, K, M));
@@ -194,13 +193,26 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
         constexpr int CPT = decltype(cpt)::value;
         using C = NormGradRowCfg<TX, TY, E, CPT>;
         constexpr auto kernel = layer_norm_grad_rows_kernel<TX, TY, E, CPT>;
-        return launch(kernel, ctas_per_sm<kernel>(C::WARPS * 32, C::SMEM), C::WARPS * 32, C::SMEM, cdiv(M, C::WARPS));
+        const int n = ctas_per_sm<kernel>(C::WARPS * 32, C::SMEM);
+        if (n < 1) return int(BL_ERR_CUDA);
+        return launch(kernel, persistent_grid(n, sms, cdiv(M, C::WARPS), most), C::WARPS * 32, C::SMEM);
       };
       auto tiles = [&](auto cpt, auto warps) {
         constexpr int CPT = decltype(cpt)::value, W = decltype(warps)::value;
         using C = NormGradTileCfg<TX, TY, E, CPT, W>;
         constexpr auto kernel = layer_norm_grad_tile_kernel<TX, TY, E, CPT, W>;
-        return launch(kernel, ctas_per_sm<kernel>(C::THREADS, C::SMEM), C::THREADS, C::SMEM, cdiv(M, C::R));
+        const int n = ctas_per_sm<kernel>(C::THREADS, C::SMEM);
+        if (n < 1) return int(BL_ERR_CUDA);
+        // rows per tile: the height whose rounds take least, a round costing its rows and about one more, the partial
+        // rows about one per 130 (777 x 1001: 13.2 us with the tallest tile, 98 CTAs of them)
+        int height = 1;
+        int64_t best = INT64_MAX, grid = 1;
+        for (int h = 1; h <= C::R; ++h) {
+          const int64_t tiles_h = cdiv(M, h), g = persistent_grid(n, sms, tiles_h, most);
+          const int64_t cost = 130 * cdiv(tiles_h, g) * (h + 1) + g;
+          if (cost <= best) best = cost, height = h, grid = g;
+        }
+        return launch(kernel, grid, C::THREADS, C::SMEM, height);
       };
       if (K <= 256) return rows(Int<8>{});
       if (K <= 512) return rows(Int<16>{});

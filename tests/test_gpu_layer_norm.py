@@ -97,6 +97,16 @@ def test_row_counts(bl, M):
         _check_backward(bl.layer_norm_backward(x.cuda(), w.cuda(), mean, rstd, dy.cuda()), x, w, dy, f"M={M}")
 
 
+@pytest.mark.parametrize("K", [640, 1001, 2050, 2304, 3500, 4999, 5000, 6000, 7001])
+@pytest.mark.parametrize("M", [1, 7, 150, 450, 1333])
+def test_tiles_of_every_height(bl, M, K):
+    """Few rows to many: the tiles of the gradient take one row to eight, the last one fewer."""
+    x, w, b, dy = _inputs(M, K, BF16, BF16, seed=M * K)
+    y, mean, rstd = _forward(bl, x, w, b, BF16)
+    _check_forward(y, mean, rstd, x, w, b, BF16, f"{M}x{K}")
+    _check_backward(bl.layer_norm_backward(x.cuda(), w.cuda(), mean, rstd, dy.cuda()), x, w, dy, f"{M}x{K}")
+
+
 @pytest.mark.parametrize("K", [256, 1000, 4096, 9000])
 def test_absent_weight_and_bias(bl, K):
     x, w, b, dy = _inputs(19, K, F32, BF16, seed=K)
