@@ -996,7 +996,7 @@ int bl_embedding(const void* ids, int id_type, const void* table, int table_type
     auto run = [&](auto ti, auto e) {
       using TI = decltype(ti);
       constexpr int E = decltype(e)::value;
-      const int64_t tiles = cdiv(D, kEmbBatch * 32 * E);
+      const int64_t tiles = cdiv(D, emb_batch(E) * 32 * E);
       if (T * tiles > int64_t(0xFFFFFFFF)) return int(BL_ERR_UNSUPPORTED);
       return launch_after(embedding_kernel<TI, TT, TY, E>, dim3(unsigned(cdiv(T * tiles, kEmbThreads / 32))), kEmbThreads,
                           0, s, static_cast<const TI*>(ids), static_cast<const TT*>(table), static_cast<TY*>(y),

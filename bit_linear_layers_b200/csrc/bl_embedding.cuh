@@ -29,9 +29,9 @@ __device__ __forceinline__ int64_t embed_row(const TI* ids, int64_t t, int64_t V
 }
 
 constexpr int kEmbThreads = 256;
-constexpr int kEmbBatch = 4;  // accesses in flight per lane
+constexpr int emb_batch(int E) { return E == 1 ? 16 : 4; }  // accesses in flight per lane
 
-// One warp per token and kEmbBatch * 32 accesses of its row; a token outside
+// One warp per token and up to 16 * 32 single elements or 4 * 32 accesses of eight; a token outside
 // the table gets a row of zeros. Bound by memory: 16384 rows of 2048 from fp32 to
 // bf16 18.2 us (93% of the copy rate; 24 us with a CTA per token and one access in
 // flight), 16 rows of 4096 1.5 us.
@@ -45,24 +45,22 @@ __global__ void __launch_bounds__(kEmbThreads)
   if (t >= T) return;
   const int64_t row = embed_row(ids, t, V);
   if (row < 0 && lane == 0 && tile == 0) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingId);
-  const int64_t k0 = static_cast<int64_t>(tile) * (kEmbBatch * 32 * E) + lane * E;
-  float f[kEmbBatch][E];
+  constexpr int BATCH = emb_batch(E);
+  const int64_t k0 = static_cast<int64_t>(tile) * (BATCH * 32 * E) + lane * E;
+  const TT* src = table + (row < 0 ? 0 : row) * D;
+  float f[BATCH][E];
+  // from valid places all of them, so that nothing stands between the loads
 #pragma unroll
-  for (int u = 0; u < kEmbBatch; ++u) {
+  for (int u = 0; u < BATCH; ++u) {
     const int64_t k = k0 + u * (32 * E);
-    if (k < D && row >= 0) {
-      Elem<TT, E>::load(table + row * D + k, f[u]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j) f[u][j] = 0.f;
-    }
+    Elem<TT, E>::load(src + (k < D ? k : D - E), f[u]);
   }
 #pragma unroll
-  for (int u = 0; u < kEmbBatch; ++u) {
+  for (int u = 0; u < BATCH; ++u) {
     const int64_t k = k0 + u * (32 * E);
     if (k < D) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) f[u][j] *= scale;
+      for (int j = 0; j < E; ++j) f[u][j] = row < 0 ? 0.f : f[u][j] * scale;
       Elem<TY, E>::store(y + static_cast<int64_t>(t) * D + k, f[u]);
     }
   }
@@ -300,8 +298,19 @@ __device__ __forceinline__ void embed_zero(uint32_t* bits, const TI* __restrict_
     for (uint32_t r = warp; r < rows; r += kEgWarps) {
       if ((bits[r >> 5] >> (r & 31)) & 1u) continue;
       TT* row = dtable + static_cast<int64_t>(v0 + r) * D;
+      if constexpr (E > 1) {
 #pragma unroll 4
-      for (int64_t k = static_cast<int64_t>(lane) * E; k < D; k += 32 * E) Elem<TT, E>::store(row + k, zero);
+        for (int64_t k = static_cast<int64_t>(lane) * E; k < D; k += 32 * E) Elem<TT, E>::store(row + k, zero);
+      } else {
+        // 16 bytes at a time between the row's first and last whole pieces, its ends one by one
+        const uintptr_t a = reinterpret_cast<uintptr_t>(row), end = a + static_cast<uintptr_t>(D) * sizeof(TT);
+        const uintptr_t a16 = min((a + 15) & ~uintptr_t(15), end), e16 = max(end & ~uintptr_t(15), a16);
+#pragma unroll 4
+        for (uintptr_t i = a16 + lane * 16; i < e16; i += 512) *reinterpret_cast<uint4*>(i) = make_uint4(0u, 0u, 0u, 0u);
+        const uintptr_t head = a + lane * sizeof(TT), tail = e16 + lane * sizeof(TT);
+        if (head < a16) Elem<TT, 1>::store(reinterpret_cast<TT*>(head), zero);
+        if (tail < end) Elem<TT, 1>::store(reinterpret_cast<TT*>(tail), zero);
+      }
     }
     __syncthreads();  // the bits are read
   }
@@ -320,15 +329,15 @@ constexpr int kEgCols = 256;   // columns per warp
 constexpr int kEgChunk = 32;   // sorted positions per warp
 constexpr int kEgShort = 8;    // ... of a list so short that chunks of 32 leave SMs without work
 
-// the row as loaded, unpacked when it is added
+// the row as loaded, unpacked when it is added; always loaded from valid places
+// (behind the last column from it), so that nothing stands between the loads
 template <typename T, int E>
 struct EgRow {
   static constexpr int NC = kEgCols / (32 * E);
   float f[NC][E];
   __device__ __forceinline__ void load(const T* row, int64_t col, int64_t D) {
 #pragma unroll
-    for (int u = 0; u < NC; ++u)
-      if (col + u * 32 * E < D) Elem<T, E>::load(row + col + u * 32 * E, f[u]);
+    for (int u = 0; u < NC; ++u) Elem<T, E>::load(row + min(col + u * 32 * E, D - E), f[u]);
   }
   __device__ __forceinline__ void add(float (&acc)[NC][E]) const {
 #pragma unroll
@@ -341,10 +350,9 @@ template <>
 struct EgRow<uint16_t, 8> {
   uint4 v;
   __device__ __forceinline__ void load(const uint16_t* row, int64_t col, int64_t D) {
-    if (col < D)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "l"(row + col));
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(row + min(col, D - 8)));
   }
   __device__ __forceinline__ void add(float (&acc)[1][8]) const {
     const uint32_t h[4] = {v.x, v.y, v.z, v.w};
@@ -437,7 +445,7 @@ __global__ void __launch_bounds__(kEgThreads, 3)
 #pragma unroll
     for (uint32_t b = 0; b < BATCH; ++b) {
       const uint32_t t = val_of(min(i0 + b, end - 1));
-      if (i0 + b < end) row[b].load(dy + static_cast<int64_t>(t) * D, col, D);
+      row[b].load(dy + static_cast<int64_t>(t) * D, col, D);
     }
 #pragma unroll
     for (uint32_t b = 0; b < BATCH; ++b) {
