@@ -14,7 +14,7 @@ import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", f) for f in ("bl_api.cu", "bl_norm.cu")]
+SRCS = [os.path.join(PKG, "csrc", f) for f in ("bl_api.cu", "bl_norm.cu", "bl_norm_grad.cu")]
 LIB = os.path.join(PKG, "libbitlinear.so")
 BINDING_SRC = os.path.join(PKG, "csrc", "bl_binding.cpp")
 BINDING = os.path.join(PKG, "_native.so")

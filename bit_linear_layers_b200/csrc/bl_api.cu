@@ -2,9 +2,9 @@
 //
 // Host side only: argument validation, per-device one-time set-up, TMA
 // descriptor encoding and kernel dispatch. The kernels live in the headers
-// included below; the layer norms have a translation unit of their own
-// (bl_norm.cu; no relocatable device code, nothing on the device is shared
-// between the two). Nothing here allocates memory.
+// included below; the layer norm and its gradient have translation units of
+// their own (bl_norm.cu, bl_norm_grad.cu; no relocatable device code, nothing on
+// the device is shared between them). Nothing here allocates memory.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -998,6 +998,12 @@ int bl_embedding(const void* ids, int id_type, const void* table, int table_type
       constexpr int E = decltype(e)::value;
       const int64_t tiles = cdiv(D, emb_batch(E) * 32 * E);
       if (T * tiles > int64_t(0xFFFFFFFF)) return int(BL_ERR_UNSUPPORTED);
+      // a warp's accesses are more than the row's: several rows to a warp
+      const int64_t n = cdiv(D, E), items = T * n;
+      if (n < 32 * emb_batch(E) / 2 && items < (int64_t(1) << 31))
+        return launch_after(embedding_narrow_kernel<TI, TT, TY, E>, dim3(unsigned(cdiv(items, kEmbThreads * 4))),
+                            kEmbThreads, 0, s, static_cast<const TI*>(ids), static_cast<const TT*>(table),
+                            static_cast<TY*>(y), uint32_t(items), uint32_t(n), V, D, scale);
       return launch_after(embedding_kernel<TI, TT, TY, E>, dim3(unsigned(cdiv(T * tiles, kEmbThreads / 32))), kEmbThreads,
                           0, s, static_cast<const TI*>(ids), static_cast<const TT*>(table), static_cast<TY*>(y),
                           uint32_t(T), V, D, uint32_t(tiles), scale);

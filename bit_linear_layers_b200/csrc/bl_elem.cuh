@@ -40,6 +40,12 @@ struct Elem<uint16_t, 4> {
   }
 };
 template <>
+struct Elem<float, 2> {
+  static __device__ __forceinline__ void store(float* p, const float (&f)[2]) {
+    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+  }
+};
+template <>
 struct Elem<float, 4> {
   static __device__ __forceinline__ void load(const float* p, float (&f)[4]) {
     const float4 v = *reinterpret_cast<const float4*>(p);
@@ -132,14 +138,14 @@ __device__ __forceinline__ float2 tree_sum2(const float2 (&f)[N]) {
 
 // ---------------------------------------------------------------------------
 // Rows of a matrix staged in shared memory by asynchronous copies, and read
-// from there E elements at a time. E = 1 takes rows of any alignment: the copy
-// keeps the row's offset within 16 bytes, so that all of it but the ends moves
-// in 16-byte pieces whatever the width of the matrix, and the elements are read
-// one by one.
+// from there E elements at a time. E = 1 takes rows of any alignment, E = 2 those
+// of an even width: the copy keeps the row's offset within 16 bytes, so that all
+// of it but the ends moves in 16-byte pieces whatever the width of the matrix.
 template <typename T, int E>
 struct StagedRow {
+  static constexpr bool OFFSET = E <= 2;            // rows keep their offset
   static constexpr int PAIRS = E == 1 ? 1 : E / 2;  // pairs of a unit (E = 1: two elements `stride` apart)
-  static constexpr int PAD = E == 1 ? 32 : 0;       // bytes of a slot beyond its columns
+  static constexpr int PAD = OFFSET ? 32 : 0;       // bytes of a slot beyond its columns
 
   // T threads (tid their index) copy K <= KP elements from g into the slot.
   // cut_head, cut_tail: the memory just ahead of / behind the row may not be read
@@ -150,7 +156,7 @@ struct StagedRow {
     constexpr int threads = T_;
     const uint32_t slot = smem_u32(slot_ptr);
     const int bytes = K * static_cast<int>(sizeof(T));
-    if constexpr (E > 1) {
+    if constexpr (!OFFSET) {
       const uint8_t* src = reinterpret_cast<const uint8_t*>(g) + tid * 16;
       constexpr int PIECES = (KP * int(sizeof(T)) + T_ * 16 - 1) / (T_ * 16);
 #pragma unroll
@@ -183,16 +189,23 @@ struct StagedRow {
   static __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   }
-  // zeros behind the row's columns, once: the copies never reach there (E > 1 only)
+  // zeros behind the row's columns, once: the copies never reach there (with an
+  // offset they do: what is read from there is replaced)
   template <int KP, int T_>
   static __device__ __forceinline__ void clear_pad(uint8_t* slot, int K, int tid) {
-    if constexpr (E > 1)
+    if constexpr (!OFFSET)
       for (int i = K * int(sizeof(T)) + tid * 16; i < KP * int(sizeof(T)); i += T_ * 16)
         *reinterpret_cast<uint4*>(slot + i) = make_uint4(0u, 0u, 0u, 0u);
   }
   // element 0 within the slot
   static __device__ __forceinline__ const uint8_t* first(const uint8_t* slot, const T* g) {
-    return E > 1 ? slot : slot + (reinterpret_cast<uintptr_t>(g) & 15u);
+    return OFFSET ? slot + (reinterpret_cast<uintptr_t>(g) & 15u) : slot;
+  }
+  // the unit with zeros behind the row's columns
+  static __device__ __forceinline__ void get_or_zero(const uint8_t* row, int k, int stride, int K, float2 (&f)[PAIRS]) {
+    get(row, k, stride, f);
+    if constexpr (E == 1) f[0] = make_float2(k < K ? f[0].x : 0.f, k + stride < K ? f[0].y : 0.f);
+    if constexpr (E == 2) f[0] = k < K ? f[0] : make_float2(0.f, 0.f);
   }
   // the unit at column k (E = 1: columns k and k + stride) of a row in shared memory
   static __device__ __forceinline__ void get(const uint8_t* row, int k, int stride, float2 (&f)[PAIRS]) {
@@ -202,6 +215,11 @@ struct StagedRow {
         f[0] = make_float2(p[0], p[stride]);
       else
         f[0] = make_float2(bf16_bits_to_float(p[0]), bf16_bits_to_float(p[stride]));
+    } else if constexpr (E == 2) {
+      if constexpr (sizeof(T) == 4)
+        f[0] = *reinterpret_cast<const float2*>(p);
+      else
+        f[0] = bf16_pair(*reinterpret_cast<const uint32_t*>(p));
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int j = 0; j < E / 4; ++j) {

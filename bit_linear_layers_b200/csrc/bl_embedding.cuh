@@ -66,6 +66,38 @@ __global__ void __launch_bounds__(kEmbThreads)
   }
 }
 
+// Rows of few columns: the output as one run of accesses, `n` to a row, so that
+// no lane is without one (65536 rows of 128 columns: 6.3 us, 14.6 us with a warp
+// to each).
+template <typename TI, typename TT, typename TY, int E>
+__global__ void __launch_bounds__(kEmbThreads)
+    embedding_narrow_kernel(const TI* __restrict__ ids, const TT* __restrict__ table, TY* __restrict__ y, uint32_t items,
+                            uint32_t n, int64_t V, int64_t D, float scale) {
+  constexpr int BATCH = 4;
+  grid_begin();
+  const uint32_t i0 = blockIdx.x * (kEmbThreads * BATCH) + threadIdx.x;
+  float f[BATCH][E];
+  int64_t row[BATCH];
+  uint32_t t[BATCH], k[BATCH];
+#pragma unroll
+  for (int u = 0; u < BATCH; ++u) {
+    const uint32_t i = min(i0 + u * kEmbThreads, items - 1);
+    t[u] = i / n;
+    k[u] = (i - t[u] * n) * E;
+    row[u] = embed_row(ids, t[u], V);
+  }
+#pragma unroll
+  for (int u = 0; u < BATCH; ++u) Elem<TT, E>::load(table + (row[u] < 0 ? 0 : row[u]) * D + k[u], f[u]);
+#pragma unroll
+  for (int u = 0; u < BATCH; ++u) {
+    if (i0 + u * kEmbThreads >= items) break;
+    if (row[u] < 0 && k[u] == 0) record_error(BL_ERR_INVALID_ARG, kWhereEmbeddingId);
+#pragma unroll
+    for (int j = 0; j < E; ++j) f[u][j] = row[u] < 0 ? 0.f : f[u][j] * scale;
+    Elem<TY, E>::store(y + static_cast<int64_t>(t[u]) * D + k[u], f[u]);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // The sort: one cluster of 8 CTAs, a stable radix sort of (id, position) by
 // digits of up to 8 bits, ping-pong through the workspace (it stays in L2).

@@ -14,7 +14,7 @@ namespace bl {
 
 // one-time set-up of the current device (bl_api.cu); *num_sms where given
 int library_device(int* num_sms);
-// bytes of workspace of bl_layer_norm_backward (bl_norm.cu)
+// bytes of workspace of bl_layer_norm_backward (bl_norm_grad.cu)
 size_t norm_workspace_bytes(int64_t M, int64_t K);
 
 namespace {
@@ -48,6 +48,16 @@ inline int check_rows(int64_t M, int64_t K, int64_t ld) {
   if (ld < K) return BL_ERR_INVALID_ARG;
   if (ld > kMaxProduct || (M > 0 && ld >= kMaxProduct / M)) return BL_ERR_UNSUPPORTED;
   return BL_OK;
+}
+
+inline int check_norm_shape(int64_t M, int64_t K) {
+  if (M < 0 || K < 1) return BL_ERR_INVALID_ARG;
+  return M > kMaxDim || K > kMaxDim ? BL_ERR_UNSUPPORTED : BL_OK;
+}
+
+// rows that `elems` elements at a time can be read or written of
+inline bool rows_aligned(const void* p, int type, int64_t ld, int64_t K, int64_t M, int elems) {
+  return K % elems == 0 && (M <= 1 || ld % elems == 0) && aligned_to(p, elems * type_bytes(type));
 }
 
 template <int V>
