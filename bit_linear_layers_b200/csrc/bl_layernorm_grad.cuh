@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
   using RowX = StagedRow<TX, E>;
   using RowG = StagedRow<TG, E>;
   constexpr int R = C::R;
-  constexpr int P = W > R ? W / R : 1, Q = R > W ? R / W : 1;  // warps to a row's sums, rows to a warp
+  constexpr int P = W > R ? W / R : 1, Q = R > W ? (R + W - 1) / W : 1;  // warps to a row's sums, rows to a warp
   constexpr int PAIRS = RowX::PAIRS, UNIT = E == 1 ? 2 : E, NU = CPT / UNIT, T = W * 32;
+  static_assert(C::KP % (P * 32 * UNIT) == 0, "a whole number of units per lane");
   constexpr int NS = C::KP / P / 32 / UNIT, TS = 32;  // the sums' units per lane and row
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float4 sums[R * P];       // of d, g and g d

@@ -28,17 +28,23 @@ int with_wide_tile(int64_t K, bool few, F&& f) {
   if (K <= 8192) return f(Int<32>{}, Int<8>{});
   return f(Int<32>{}, Int<16>{});
 }
-// Rows of any alignment, read element by element: 16 columns per thread, in
-// finer steps, since a thread without columns costs as much as one with them
-// (5001 columns: 22 us in a tile of 8192, 14 us in one of 5120). Reading even
+// Rows of any alignment, read element by element: up to 16 columns per thread,
+// in finer steps, since a thread without columns costs as much as one with them
+// (1537 x 5001: 22 us in a tile of 8192, 14 us in one of 5120), and as few warps
+// as that allows (30000 x 301: 43 us with four, 20 us with one). Reading even
 // widths in pairs gains nothing here (4096 x 2050: 17 and 17 us from bf16, 21 and
 // 19 us from fp32); the gradient does so.
 template <typename F>
 int with_narrow_tile(int64_t K, F&& f) {
   if (K <= 256) return f(Int<8>{}, Int<1>{});
-  if (K <= 1024) return f(Int<8>{}, Int<4>{});
+  if (K <= 384) return f(Int<12>{}, Int<1>{});
+  if (K <= 512) return f(Int<16>{}, Int<1>{});
+  if (K <= 768) return f(Int<12>{}, Int<2>{});
+  if (K <= 1024) return f(Int<16>{}, Int<2>{});
+  if (K <= 1536) return f(Int<16>{}, Int<3>{});
   if (K <= 2048) return f(Int<16>{}, Int<4>{});
   if (K <= 2560) return f(Int<16>{}, Int<5>{});
+  if (K <= 3584) return f(Int<16>{}, Int<7>{});
   if (K <= 4096) return f(Int<16>{}, Int<8>{});
   if (K <= 5120) return f(Int<16>{}, Int<10>{});
   if (K <= 6144) return f(Int<16>{}, Int<12>{});

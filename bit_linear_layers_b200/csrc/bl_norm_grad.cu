@@ -125,7 +125,11 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
       };
       if (K <= 256) return rows(Int<8>{});
       if (K <= 512) return rows(Int<16>{});
+      if constexpr (E <= 2)  // read element by element a column without data costs as much as any: a finer step
+        if (K <= 768) return tiles(Int<6>{}, Int<4>{});
       if (K <= 1024) return tiles(Int<8>{}, Int<4>{});
+      if constexpr (E <= 2)
+        if (K <= 1536) return tiles(Int<8>{}, Int<6>{});
       if (K <= 2048) return tiles(Int<8>{}, Int<8>{});
       if (K <= 2560) return tiles(Int<8>{}, Int<10>{});
       if (K <= 4096) return tiles(Int<8>{}, Int<16>{});

@@ -97,7 +97,7 @@ def test_row_counts(bl, M):
         _check_backward(bl.layer_norm_backward(x.cuda(), w.cuda(), mean, rstd, dy.cuda()), x, w, dy, f"M={M}")
 
 
-@pytest.mark.parametrize("K", [640, 1001, 2050, 2304, 3500, 4999, 5000, 6000, 7001])
+@pytest.mark.parametrize("K", [301, 640, 701, 766, 1001, 1501, 1530, 2050, 2304, 3500, 4999, 5000, 6000, 7001])
 @pytest.mark.parametrize("M", [1, 7, 150, 450, 1333])
 def test_tiles_of_every_height(bl, M, K):
     """Few rows to many: the tiles of the gradient take one row to eight, the last one fewer."""
