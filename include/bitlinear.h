@@ -369,8 +369,7 @@ int bl_embedding(const void* ids, int id_type, const void* table, int table_type
 
 /*
  * bl_embedding_backward -- the gradient of the whole table:
- *   dtable_v = scale * sum_{t: ids_t = v} dy_t      (fp32 sums, in the order of t
- *                                                    within runs of 32 sorted tokens)
+ *   dtable_v = scale * sum_{t: ids_t = v} dy_t      (fp32 sums, always in the same order)
  * dy [T x D] of dy_type, dtable [V x D] of table_type. Rows that no token
  * names are zero-filled. With BL_EMBED_ACCUMULATE the sums are added to
  * dtable instead, and rows that no token names are not touched (a table that
