@@ -1196,7 +1196,6 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
       return st;
     };
     // descriptors are copied with each launch: no more of them than there are
-    // descriptors are copied with each launch: no more of them than there are
     if (num_tensors <= 32) return run(Int<32>{});
     return num_tensors <= 256 ? run(Int<256>{}) : run(Int<kGcMaxTensors>{});
   } catch (...) {  // out of host memory

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256)
     slot = slot + 1 == S ? 0 : slot + 1;
   }
   grid_dependents_launch();  // the kernel that adds the partial rows up may be scheduled; it waits for them
-  if (!part) return;  // the kernel that adds the partial rows up may be scheduled; it waits for them
+  if (!part) return;
   cp_async_wait<0>();
   __syncthreads();  // the ring is free: the warps' sums meet there
   float* acc = reinterpret_cast<float*>(smem);  // [warp][dweight | dbias][KP]
