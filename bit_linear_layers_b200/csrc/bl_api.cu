@@ -1122,12 +1122,17 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
     if (!std::is_sorted(outs.begin(), outs.end(), before)) std::sort(outs.begin(), outs.end(), before);
     for (size_t j = 1; j < outs.size(); ++j)
       if (outs[j].a < outs[j - 1].b) return BL_ERR_INVALID_ARG;
+    // j: the outs that begin below the end of a gradient; in one order mostly, so the next is near
+    const auto below = [](const Range& l, uintptr_t v) { return l.a < v; };
+    size_t j = 0;
     for (int i = 0; i < num_tensors && !outs.empty(); ++i) {
       const bl_grad_tensor& t = tensors[i];
       if (t.numel == 0) continue;
       const uintptr_t a = reinterpret_cast<uintptr_t>(t.g), b = a + uintptr_t(t.numel) * uintptr_t(type_bytes(t.type));
-      auto it = std::lower_bound(outs.begin(), outs.end(), b, [](const Range& l, uintptr_t v) { return l.a < v; });
-      if (it != outs.begin() && (it - 1)->b > a && ((it - 1)->a != a || (it - 1)->i != i)) return BL_ERR_INVALID_ARG;
+      if (j > 0 && outs[j - 1].a >= b) j = 0;
+      for (int near = 0; near < 4 && j < outs.size() && outs[j].a < b; ++near) ++j;
+      if (j < outs.size() && outs[j].a < b) j = size_t(std::lower_bound(outs.begin() + j, outs.end(), b, below) - outs.begin());
+      if (j > 0 && outs[j - 1].b > a && (outs[j - 1].a != a || outs[j - 1].i != i)) return BL_ERR_INVALID_ARG;
     }
     int sms = 0;
     const int rc = device_setup(&sms);
@@ -1138,7 +1143,8 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
     // launches of up to CAP tensors: all the norms, then all the products
     auto run = [&](auto cap) {
       constexpr int CAP = decltype(cap)::value;
-      static thread_local GcParams<CAP> P;
+      static thread_local GcParams<CAP> table;
+      GcParams<CAP>& P = table;
       int chunks = 0, grid = 1;
       bool writes = false;
       // the tensors of a launch that begins at tensor i; returns where the next one begins
@@ -1161,12 +1167,15 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
         P.chunk0[n] = static_cast<int32_t>(total_chunks);
         chunks = static_cast<int>(total_chunks);
         grid = std::max(1, std::min(chunks, ctas));
+        // the tensor of each CTA's first chunk; behind them all, of the last chunk
         const int q = chunks / grid, r = chunks % grid;
-        for (int b = 0, c = 0, at = 0; b <= grid; ++b) {
-          while (at + 1 < n && P.chunk0[at + 1] <= c) ++at;
-          P.first[b] = static_cast<uint16_t>(at);
-          c = std::min(c + q + (b < r ? 1 : 0), std::max(0, chunks - 1));
-        }
+        int b = 0, c = 0;
+        for (int at = 0; at < n; ++at)
+          for (const int e = P.chunk0[at + 1]; c < e && b < grid; ++b) {
+            P.first[b] = static_cast<uint16_t>(at);
+            c += q + (b < r ? 1 : 0);
+          }
+        P.first[grid] = static_cast<uint16_t>(std::max(0, n - 1));
         return i;
       };
       int num_sums = 0;
