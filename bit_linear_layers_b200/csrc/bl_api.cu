@@ -1107,7 +1107,7 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
     };
     std::vector<Range> outs;
     outs.reserve(size_t(num_tensors));
-    int64_t total = 0;
+    int64_t total = 0, total_bytes = 0;
     for (int i = 0; i < num_tensors; ++i) {
       const bl_grad_tensor& t = tensors[i];
       if (!type_ok(t.type) || t.numel < 0) return BL_ERR_INVALID_ARG;
@@ -1115,6 +1115,7 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
       const int es = type_bytes(t.type);
       if (!t.g || !aligned_to(t.g, es) || !aligned_to(t.out, es)) return BL_ERR_INVALID_ARG;
       if (t.numel >= kMaxProduct || (total += t.numel) >= kMaxProduct) return BL_ERR_UNSUPPORTED;
+      total_bytes += t.numel * es;
       const uintptr_t o = reinterpret_cast<uintptr_t>(t.out);
       if (t.out) outs.push_back(Range{o, o + uintptr_t(t.numel) * uintptr_t(es), i});
     }
@@ -1141,8 +1142,8 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
     double* sums = static_cast<double*>(ws);
     const int ctas = std::min(sms * 8, kGcMaxCtas);
     // launches of up to CAP tensors: all the norms, then all the products
-    auto run = [&](auto cap) {
-      constexpr int CAP = decltype(cap)::value;
+    auto run = [&](auto cap, auto vecs) {
+      constexpr int CAP = decltype(cap)::value, VECS = decltype(vecs)::value;
       static thread_local GcParams<CAP> table;
       GcParams<CAP>& P = table;
       int chunks = 0, grid = 1;
@@ -1160,7 +1161,7 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
           P.f32[n] = t.type == BL_TYPE_F32;
           P.chunk0[n] = static_cast<int32_t>(total_chunks);
           const int64_t mis = int64_t(reinterpret_cast<uintptr_t>(t.g) & 15u) / es;
-          total_chunks += cdiv(t.numel + mis, int64_t(kGcChunkVecs) * 16 / es);
+          total_chunks += cdiv(t.numel + mis, int64_t(kGcThreads * VECS) * 16 / es);
           writes |= t.out != nullptr;
           ++n;
         }
@@ -1180,13 +1181,13 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
       };
       int num_sums = 0;
       auto norm = [&] {
-        const int st = launch_after(grad_norm_kernel<CAP>, dim3(unsigned(grid)), kGcThreads, 0, s, P, chunks, sums + num_sums);
+        const int st = launch_after(grad_norm_kernel<CAP, VECS>, dim3(unsigned(grid)), kGcThreads, 0, s, P, chunks, sums + num_sums);
         num_sums += grid;
         return st;
       };
       auto scale = [&](bool first) {
         if (!writes && !first) return int(BL_OK);
-        return launch_after(grad_scale_kernel<CAP>, dim3(writes ? unsigned(grid) : 1u), kGcThreads, 0, s, P,
+        return launch_after(grad_scale_kernel<CAP, VECS>, dim3(writes ? unsigned(grid) : 1u), kGcThreads, 0, s, P,
                             writes ? chunks : 0, static_cast<const double*>(sums), num_sums, max_norm,
                             first ? stats : nullptr);
       };
@@ -1205,8 +1206,11 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
       return st;
     };
     // descriptors are copied with each launch: no more of them than there are
-    if (num_tensors <= 32) return run(Int<32>{});
-    return num_tensors <= 256 ? run(Int<256>{}) : run(Int<kGcMaxTensors>{});
+    auto by_size = [&](auto cap) {
+      return total_bytes >= kGcManyBytes ? run(cap, Int<kGcVecsMany>{}) : run(cap, Int<kGcVecs>{});
+    };
+    if (num_tensors <= 32) return by_size(Int<32>{});
+    return num_tensors <= 256 ? by_size(Int<256>{}) : by_size(Int<kGcMaxTensors>{});
   } catch (...) {  // out of host memory
     return BL_ERR_CUDA;
   }

@@ -199,3 +199,24 @@ def test_refusals(bl):
         with pytest.raises(bl.BitLinearError):
             call()
     assert torch.equal(t, keep)
+
+
+@pytest.mark.parametrize("count", [3, 100, 1100])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_bytes(bl, dtype, count):
+    """From 96 MB of gradients on: ragged slices of one buffer that begin anywhere, in place; what lies around them
+    keeps its value."""
+    n = (100 << 20) // (2 if dtype == BF16 else 4)
+    cuts = np.sort(np.random.default_rng(count).integers(0, n, count - 1))
+    sizes = np.diff(np.concatenate([[0], cuts, [n]])).tolist()
+    flat = torch.randn(n + 12, generator=torch.Generator("cuda").manual_seed(count), device="cuda").to(dtype)
+    flat[:3], flat[n + 3:] = 7.0, 7.0
+    src = flat[3:n + 3].clone()
+    norm, coef = bl.grad_clip(list(flat[3:n + 3].split(sizes)), 100.0)
+    ref_norm = float(src.double().square_().sum().sqrt())
+    ref_coef = 100.0 / (ref_norm + 1e-6)
+    assert abs(float(norm) - ref_norm) <= R.NORM_REL * ref_norm and abs(float(coef) - ref_coef) <= R.COEF_REL * ref_coef
+    ref = src.double().mul_(ref_coef)
+    off = (flat[3:n + 3].double() - ref).abs_()
+    assert bool((off <= (R.COEF_REL + R.U + R.half_step(dtype)) * ref.abs() + 2.0 ** -133).all())
+    assert bool((flat[:3] == 7).all()) and bool((flat[n + 3:] == 7).all())
