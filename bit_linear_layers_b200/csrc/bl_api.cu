@@ -1052,7 +1052,8 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
   while ((V >> bits) != 0) ++bits;
   const int passes = (bits + 7) / 8, digit_bits = (bits + passes - 1) / passes;
   const uint32_t t32 = static_cast<uint32_t>(T), v32 = static_cast<uint32_t>(V);
-  const uint2* list = p.list[(passes + 1) & 1];
+  const bool sorts = T > kErMost;
+  const uint2* list = p.list[sorts ? (passes + 1) & 1 : 0];
   // writers of zeros, on the SMs that do not sort, with rows for each of their warps: four to an SM, or three of a
   // long list, which each of them reads (2048 tokens x 2048 columns: 48.7 and 52.4 us; 65536 x 256: 70 and 64 us)
   const int64_t zero_most = int64_t(T <= 8192 ? 4 : 3) * std::max(1, sms - kEsCluster);
@@ -1063,10 +1064,10 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
   auto run = [&](auto ti) {
     using TI = decltype(ti);
     const auto* id = static_cast<const TI*>(ids);
-    const bool one = T <= kEsOneCta;
-    const int st = launch_after(one ? embed_sort_kernel<TI, 1> : embed_sort_kernel<TI, kEsCluster>,
-                                dim3(one ? 1u : unsigned(kEsCluster)), kEsThreads, 0, s, id, t32, v32, padding_id, passes,
-                                digit_bits, chunk, p);
+    const int st = sorts ? launch_after(embed_sort_kernel<TI>, dim3(unsigned(kEsCluster)), kEsThreads, 0, s, id, t32, v32,
+                                        padding_id, passes, digit_bits, p)
+                         : launch_after(embed_rank_kernel<TI>, dim3(unsigned(cdiv(T, 32))), kErThreads, 0, s, id, t32, v32,
+                                        padding_id, p);
     if (st != BL_OK) return st;
     return with_types(dy_type, table_type, [&](auto tg, auto tt) {
       using TG = decltype(tg);
@@ -1078,7 +1079,8 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
         constexpr auto by_8 = embed_grad_kernel<TI, TG, TT, E, kEgShort, ACC>;
         auto* out = static_cast<TT*>(dtable);
         const int st2 = launch_after(w.chunk == kEgChunk ? by_32 : by_8, dim3(grid), kEgThreads, 0, s, id, padding_id,
-                                     zero_ctas, list, static_cast<const TG*>(dy), out, part, t32, v32, D, scale);
+                                     zero_ctas, list, static_cast<const TG*>(dy), out, part, p.num_heavy, p.heavy, p.room, t32, v32, D,
+                                     scale);
         if (st2 != BL_OK || w.chunks < 3) return st2;  // a long segment spans three chunks
         constexpr int HE = E == 8 ? 4 : 1;
         const int64_t most = cdiv((w.chunks / 2) * cdiv(D, 32 * HE), kEhWarps);
