@@ -23,6 +23,10 @@ struct Elem<float, 1> {
 };
 template <>
 struct Elem<uint16_t, 2> {
+  static __device__ __forceinline__ void load(const uint16_t* p, float (&f)[2]) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    f[0] = __uint_as_float(v << 16), f[1] = __uint_as_float(v & 0xFFFF0000u);
+  }
   static __device__ __forceinline__ void store(uint16_t* p, const float (&f)[2]) {
     *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f[0], f[1]);
   }
@@ -41,6 +45,10 @@ struct Elem<uint16_t, 4> {
 };
 template <>
 struct Elem<float, 2> {
+  static __device__ __forceinline__ void load(const float* p, float (&f)[2]) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    f[0] = v.x, f[1] = v.y;
+  }
   static __device__ __forceinline__ void store(float* p, const float (&f)[2]) {
     *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
   }

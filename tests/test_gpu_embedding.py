@@ -277,3 +277,36 @@ def test_refusals(bl):
             call()
     with pytest.raises(bl.BitLinearError):
         bl.embedding_backward(ids, dy, 5, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("tt,yt", TYPES)
+@pytest.mark.parametrize("D", [510, 511, 512, 514, 516, 1028, 2050, 2060, 2071])
+def test_widths(bl, D, tt, yt):
+    """Accesses of one, two, four and eight elements, with and without columns behind the last whole tile."""
+    V, T = 60, 333
+    ids = _zipf(T, V, D).cuda()
+    table = torch.randn(V, D, generator=_gen(D)).to(tt).cuda()
+    out, buf, s = guarded_empty((T, D), yt, "cuda")
+    assert torch.equal(bl.embedding(ids, table, scale=3.0, out=out), _plain(ids, table, 3.0, yt))
+    assert guards_intact(buf, T * D, sentinel=s)
+    _check_grad(bl, ids.cpu(), torch.randn(T, D, generator=_gen(D + 1)).to(yt), V, tt, scale=0.7)
+    _check_grad(bl, ids.cpu(), torch.randn(T, D, generator=_gen(D + 2)).to(yt), V, tt, accumulate=True)
+
+
+@pytest.mark.parametrize("T", [127, 128, 129, 4095, 4735, 4736, 4737, 6000])
+@pytest.mark.parametrize("V", [3, 5000])
+def test_lists_of_any_length(bl, T, V):
+    """On both sides of where counting gives way to sorting. Small integers: every sum is exact, and a token's rows
+    are added whichever way it is."""
+    D = 33
+    ids = _zipf(T, V, T + V)
+    dy = torch.randint(-4, 5, (T, D), generator=_gen(T)).float()
+    for it in (torch.int32, torch.int64):
+        got = bl.embedding_backward(ids.to(it).cuda(), dy.cuda(), V)
+        assert torch.equal(got.cpu(), torch.zeros(V, D).index_add_(0, ids, dy))
+    bad = ids.clone()
+    bad[T // 2], bad[T - 1] = -1, V
+    keep = (bad >= 0) & (bad < V) & (bad != ids[0])
+    got = bl.embedding_backward(bad.cuda(), dy.cuda(), V, padding_id=int(ids[0]))
+    assert torch.equal(got.cpu(), torch.zeros(V, D).index_add_(0, ids[keep], dy[keep]))
+    assert bl.device_error()[0] != 0 and bl.device_error() == (0, 0)
