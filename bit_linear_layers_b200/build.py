@@ -62,7 +62,8 @@ def build_binding(out: str = BINDING) -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-isystem{p}" if p != INCLUDE else f"-I{p}" for p in inc), "-o", out, BINDING_SRC,
-           f"-L{PKG}", "-l:libbitlinear.so", *(f"-L{p}" for p in libs), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           f"-L{PKG}", "-l:libbitlinear.so", *(f"-L{p}" for p in libs), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch", "-ltorch_python",
            "-Wl,-rpath,$ORIGIN", *(f"-Wl,-rpath,{p}" for p in libs)]
     subprocess.run(cmd, check=True)
     return out

@@ -1003,7 +1003,9 @@ int bl_embedding(const void* ids, int id_type, const void* table, int table_type
                           uint32_t(T), V, D, uint32_t(tiles), scale);
     };
     auto of_ids = [&](auto e) { return id_type == BL_IDS_I64 ? run(int64_t{}, e) : run(int32_t{}, e); };
-    const auto whole = [&](int e) { return rows_aligned(table, table_type, D, D, V, e) && rows_aligned(y, y_type, D, D, T, e); };
+    const auto whole = [&](int e) {
+      return rows_aligned(table, table_type, D, D, V, e) && rows_aligned(y, y_type, D, D, T, e);
+    };
     // as wide as both sides allow (33578 rows from fp32 to bf16: 2056 columns 32 us, 2060 33, 2050 40, 2071 44)
     if (whole(8)) return of_ids(Int<8>{});
     if (whole(4)) return of_ids(Int<4>{});
@@ -1137,7 +1139,8 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
       const uintptr_t a = reinterpret_cast<uintptr_t>(t.g), b = a + uintptr_t(t.numel) * uintptr_t(type_bytes(t.type));
       if (j > 0 && outs[j - 1].a >= b) j = 0;
       for (int near = 0; near < 4 && j < outs.size() && outs[j].a < b; ++near) ++j;
-      if (j < outs.size() && outs[j].a < b) j = size_t(std::lower_bound(outs.begin() + j, outs.end(), b, below) - outs.begin());
+      if (j < outs.size() && outs[j].a < b)
+        j = size_t(std::lower_bound(outs.begin() + j, outs.end(), b, below) - outs.begin());
       if (j > 0 && outs[j - 1].b > a && (outs[j - 1].a != a || outs[j - 1].i != i)) return BL_ERR_INVALID_ARG;
     }
     int sms = 0;
@@ -1186,7 +1189,8 @@ int bl_grad_clip(const bl_grad_tensor* tensors, int num_tensors, float max_norm,
       };
       int num_sums = 0;
       auto norm = [&] {
-        const int st = launch_after(grad_norm_kernel<CAP, VECS>, dim3(unsigned(grid)), kGcThreads, 0, s, P, chunks, sums + num_sums);
+        const int st = launch_after(grad_norm_kernel<CAP, VECS>, dim3(unsigned(grid)), kGcThreads, 0, s, P, chunks,
+                                    sums + num_sums);
         num_sums += grid;
         return st;
       };

@@ -429,8 +429,8 @@ struct EgRow<uint16_t, 8> {
 // serialisation: the zeros are written while the list is sorted.
 template <typename TG, typename TT, int E, int CH, bool ACC>
 __global__ void __launch_bounds__(kEgThreads, 3)
-    embed_grad_kernel(const void* __restrict__ ids, bool ids64, int64_t padding_id, uint32_t zero_ctas, const uint2* __restrict__ list,
-                      const TG* __restrict__ dy, TT* __restrict__ dtable, float* __restrict__ part,
+    embed_grad_kernel(const void* __restrict__ ids, bool ids64, int64_t padding_id, uint32_t zero_ctas,
+                      const uint2* __restrict__ list, const TG* __restrict__ dy, TT* __restrict__ dtable, float* __restrict__ part,
                       uint32_t* __restrict__ num_heavy, EmbedHeavy* __restrict__ heavy, uint32_t room, uint32_t T,
                       uint32_t V, int64_t D, float scale) {
   grid_dependents_launch();

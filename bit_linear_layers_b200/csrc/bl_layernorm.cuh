@@ -55,6 +55,14 @@ struct NormCfg {
   static constexpr int smem(int groups) { return WB + groups * S * SLOT; }
 };
 
+// The mean to keep. Values of few bits (bf16) differ from c by numbers that all
+// round the same way within a binade, so md has a bias of up to half a step of
+// the deviations: the correction is better than the sum's rounding only where the
+// mean is larger than they are (4 x 13056 bf16, means of 0.02 deviations: relative
+// errors of 1e-7, with the correction 2e-6). What is left of the mean is taken out
+// of z and, from the kept mean, in the gradient all the same.
+__device__ __forceinline__ float kept_mean(float c, float md, float var) { return c * c > var ? c + md : c; }
+
 // place of column k among the planes
 template <int E>
 __device__ __forceinline__ int wb_at(int k, int kp) {
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__((NormCfg<TX, E, CPT, W>::GROUPS * W * 32))
     var = var < 0.f ? 0.f : var;  // a rounding below zero; NaN stays NaN
     const float r = inv_sqrt(var + eps);
     if (tid == 0) {
-      if (mean) mean[m] = c + md;
+      if (mean) mean[m] = kept_mean(c, md, var);
       if (rstd) rstd[m] = r;
     }
     const float2 shift = both(-md * r);
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(kNormThreads)
   var = var < 0.f ? 0.f : var;  // a rounding below zero; NaN stays NaN
   const float r = inv_sqrt(var + eps);
   if (threadIdx.x == 0) {
-    if (mean) mean[m] = c + md;
+    if (mean) mean[m] = kept_mean(c, md, var);
     if (rstd) rstd[m] = r;
   }
   for (int64_t k = threadIdx.x; k < K; k += kNormThreads) {

@@ -314,3 +314,15 @@ def test_refusals(bl):
     for call in (lambda: bl.layer_norm(x, w, eps=0.0), lambda: bl.layer_norm_backward(x, w, s, s, x, dx=x)):
         with pytest.raises(bl.BitLinearError):
             call()
+
+
+@pytest.mark.parametrize("K", [100, 512, 1001, 4096, 13056, 20000])
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_mean_near_zero(bl, K, xt):
+    """Eighths between -4 and 4: their sums are exact in any order, so the kept mean is off by the roundings of 1 / K
+    and of the product alone, however coarse the values are."""
+    x = (torch.randint(-32, 33, (37, K), generator=torch.Generator().manual_seed(K)) / 8.0).to(xt)
+    mean = bl.layer_norm(x.cuda(), stats=True)[1]
+    ref = R.f64(x).mean(1)
+    assert (ref ** 2 < R.f64(x).var(1)).all()
+    R.check(mean, ref, 2.01 * R.U * np.abs(ref), "mean")
