@@ -386,73 +386,96 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
 }
 
 // Rows too long for that: dx and the weight's gradient separately, from two
-// readings of x and dy. One CTA per row: dx (where wanted) and the row's correction of the kept mean.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(kNormThreads)
+// readings of x and dy, E elements per access. One CTA per row: dx (where wanted) and
+// the row's correction of the kept mean.
+constexpr int kNormLongThreads = 512;
+
+template <typename TX, typename TY, int E>
+__global__ void __launch_bounds__(kNormLongThreads)
     layer_norm_dx_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ w,
                          const float* __restrict__ mean, const float* __restrict__ rstd, const TY* __restrict__ dy,
                          int64_t lddy, TX* __restrict__ dx, int64_t lddx, float* __restrict__ shift, int64_t K) {
-  __shared__ float sh[3 * kNormWarps];
+  constexpr int WARPS = kNormLongThreads / 32;
+  __shared__ float sh[3 * WARPS];
   grid_begin();
   const int64_t m = blockIdx.x;
   const TX* xr = x + m * ldx;
   const TY* gr = dy + m * lddy;
   const float c = mean[m], r = rstd[m];
   float s[3] = {0.f, 0.f, 0.f};  // sums of d, g and g d
-  float fx[1], fg[1];
-  for (int64_t k = threadIdx.x; k < K; k += kNormThreads) {
-    Elem<TX, 1>::load(xr + k, fx);
-    Elem<TY, 1>::load(gr + k, fg);
-    const float d = fx[0] - c, g = w ? fg[0] * w[k] : fg[0];
-    s[0] += d;
-    s[1] += g;
-    s[2] = fmaf(g, d, s[2]);
+#pragma unroll 4
+  for (int64_t k = threadIdx.x * E; k < K; k += kNormLongThreads * E) {
+    float fx[E], fg[E];
+    Elem<TX, E>::load(xr + k, fx);
+    Elem<TY, E>::load(gr + k, fg);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float d = fx[j] - c, g = w ? fg[j] * w[k + j] : fg[j];
+      s[0] += d;
+      s[1] += g;
+      s[2] = fmaf(g, d, s[2]);
+    }
   }
-  block_sums<kNormWarps>(s, sh);
+  block_sums<WARPS>(s, sh);
   const float inv_k = 1.0f / static_cast<float>(K);
   const float md = s[0] * inv_k;
   const float mg = s[1] * inv_k, mgz = r * (s[2] - md * s[1]) * inv_k;
   if (shift && threadIdx.x == 0) shift[m] = md;
   if (!dx) return;
-  for (int64_t k = threadIdx.x; k < K; k += kNormThreads) {
-    Elem<TX, 1>::load(xr + k, fx);
-    Elem<TY, 1>::load(gr + k, fg);
-    const float z = ((fx[0] - c) - md) * r, g = w ? fg[0] * w[k] : fg[0];
-    fx[0] = r * (g - mg - z * mgz);
-    Elem<TX, 1>::store(dx + m * lddx + k, fx);
+#pragma unroll 4
+  for (int64_t k = threadIdx.x * E; k < K; k += kNormLongThreads * E) {
+    float fx[E], fg[E];
+    Elem<TX, E>::load(xr + k, fx);
+    Elem<TY, E>::load(gr + k, fg);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float z = ((fx[j] - c) - md) * r, g = w ? fg[j] * w[k + j] : fg[j];
+      fx[j] = r * (g - mg - z * mgz);
+    }
+    Elem<TX, E>::store(dx + m * lddx + k, fx);
   }
 }
 
 // Partial sums of dy z and dy over the rows m = p, p + P, ...: CTA (column
-// block, p), one column per lane, the rows dealt to the warps.
-template <typename TX, typename TY>
+// block, p), E columns per lane, the rows dealt to the warps, four in flight.
+template <typename TX, typename TY, int E>
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_dw_kernel(const TX* __restrict__ x, int64_t ldx, const float* __restrict__ mean,
                          const float* __restrict__ rstd, const float* __restrict__ shift, const TY* __restrict__ dy,
                          int64_t lddy, float* __restrict__ part, int64_t M, int64_t K) {
-  __shared__ float sh[2][kNormWarps][32];
+  __shared__ float sh[2][kNormWarps][32 * E];
   grid_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * (32 * E), k = k0 + lane * E;
   const int64_t p = blockIdx.y, P = gridDim.y;
-  float sw = 0.f, sb = 0.f;
+  float sw[E] = {}, sb[E] = {};
   if (k < K) {
-    float fx[1], fg[1];
+#pragma unroll 4
     for (int64_t m = p + warp * P; m < M; m += P * kNormWarps) {
-      Elem<TX, 1>::load(x + m * ldx + k, fx);
-      Elem<TY, 1>::load(dy + m * lddy + k, fg);
-      sw = fmaf(fg[0], ((fx[0] - mean[m]) - shift[m]) * rstd[m], sw);
-      sb += fg[0];
+      float fx[E], fg[E];
+      Elem<TX, E>::load(x + m * ldx + k, fx);
+      Elem<TY, E>::load(dy + m * lddy + k, fg);
+      const float c = mean[m], md = shift[m], r = rstd[m];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        sw[j] = fmaf(fg[j], ((fx[j] - c) - md) * r, sw[j]);
+        sb[j] += fg[j];
+      }
     }
   }
-  sh[0][warp][lane] = sw;
-  sh[1][warp][lane] = sb;
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    sh[0][warp][j * 32 + lane] = sw[j];
+    sh[1][warp][j * 32 + lane] = sb[j];
+  }
   __syncthreads();
-  if (warp < 2 && k < K) {
+  for (int i = threadIdx.x; i < 64 * E; i += kNormThreads) {
+    const int which = i / (32 * E), col = i % (32 * E);
+    if (k0 + col >= K) continue;
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < kNormWarps; ++i) t += sh[warp][i][lane];
-    part[(warp * P + p) * K + k] = t;
+    for (int v = 0; v < kNormWarps; ++v) t += sh[which][v][(col % E) * 32 + col / E];
+    part[(which * P + p) * K + k0 + col] = t;
   }
 }
 

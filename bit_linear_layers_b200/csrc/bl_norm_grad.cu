@@ -78,24 +78,30 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
       return launch_after(layer_norm_dw_sum_kernel, dim3(unsigned(cdiv(K, 32)), 2), kNormSumThreads, 0, s,
                           static_cast<const float*>(part), int(parts), K, dweight, dbias);
     };
-    if (K > kNormGradMaxK) {
-      int st = launch_after(layer_norm_dx_kernel<TX, TY>, dim3(unsigned(M)), kNormThreads, 0, s, xp, ldx, weight, mean,
-                            rstd, gp, lddy, dxp, lddx, shift, K);
-      if (st != BL_OK || !want_dw) return st;
-      const int64_t parts = std::min<int64_t>(cdiv(M, 64), 128);
-      st = launch_after(layer_norm_dw_kernel<TX, TY>, dim3(unsigned(cdiv(K, 32)), unsigned(parts)), kNormThreads, 0, s, xp,
-                        ldx, mean, rstd, static_cast<const float*>(shift), gp, lddy, part, M, K);
-      return st != BL_OK ? st : sum_parts(parts);
-    }
+    constexpr int WIDE = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
+    const bool wide = rows_in_pieces(x, x_type, ldx, K, M) && rows_in_pieces(dy, dy_type, lddy, K, M) &&
+                      (!dx || rows_in_pieces(dx, x_type, lddx, K, M));
+    // even widths in pairs (4096 x 2050: 28 us, element by element 30 to 32 us)
+    const bool pairs = rows_aligned(x, x_type, ldx, K, M, 2) && rows_aligned(dy, dy_type, lddy, K, M, 2) &&
+                       (!dx || rows_aligned(dx, x_type, lddx, K, M, 2));
+    auto in_width = [&](auto f) { return wide ? f(Int<WIDE>{}) : pairs ? f(Int<2>{}) : f(Int<1>{}); };
+    if (K > kNormGradMaxK)
+      return in_width([&](auto e) {
+        constexpr int E = decltype(e)::value;
+        int st = launch_after(layer_norm_dx_kernel<TX, TY, E>, dim3(unsigned(M)), kNormLongThreads, 0, s, xp, ldx, weight,
+                              mean, rstd, gp, lddy, dxp, lddx, shift, K);
+        if (st != BL_OK || !want_dw) return st;
+        const int64_t parts = std::min<int64_t>(cdiv(M, 32), 128);
+        st = launch_after(layer_norm_dw_kernel<TX, TY, E>, dim3(unsigned(cdiv(K, 32 * E)), unsigned(parts)), kNormThreads,
+                          0, s, xp, ldx, mean, rstd, static_cast<const float*>(shift), gp, lddy, part, M, K);
+        return st != BL_OK ? st : sum_parts(parts);
+      });
     auto launch = [&](auto kernel, int64_t grid, int threads, int smem, auto... more) {
       const int st = launch_after(kernel, dim3(unsigned(grid)), threads, smem, s, xp, ldx, weight, mean, rstd, gp, lddy,
                                   dxp, lddx, part, M, int(K), more...);
       return st != BL_OK || !want_dw ? st : sum_parts(grid);
     };
     const int64_t most = want_dw ? w.parts : kMaxDim;
-    constexpr int WIDE = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
-    const bool wide = rows_in_pieces(x, x_type, ldx, K, M) && rows_in_pieces(dy, dy_type, lddy, K, M) &&
-                      (!dx || rows_in_pieces(dx, x_type, lddx, K, M));
     auto by_width = [&](auto e) {
       constexpr int E = decltype(e)::value;
       auto rows = [&](auto cpt) {
@@ -137,11 +143,7 @@ int bl_layer_norm_backward(const void* x, int x_type, int64_t ldx, const float* 
       if (K <= 6144) return tiles(Int<16>{}, Int<12>{});
       return tiles(Int<32>{}, Int<8>{});
     };
-    if (wide) return by_width(Int<WIDE>{});
-    // even widths in pairs (4096 x 2050: 28 us, element by element 30 to 32 us)
-    const bool pairs = rows_aligned(x, x_type, ldx, K, M, 2) && rows_aligned(dy, dy_type, lddy, K, M, 2) &&
-                       (!dx || rows_aligned(dx, x_type, lddx, K, M, 2));
-    return pairs ? by_width(Int<2>{}) : by_width(Int<1>{});
+    return in_width(by_width);
   });
 }
 

@@ -326,3 +326,13 @@ def test_mean_near_zero(bl, K, xt):
     ref = R.f64(x).mean(1)
     assert (ref ** 2 < R.f64(x).var(1)).all()
     R.check(mean, ref, 2.01 * R.U * np.abs(ref), "mean")
+
+
+@pytest.mark.parametrize("M,K", [(1, 8200), (5, 8194), (70, 8193), (300, 8448), (33, 16400)])
+@pytest.mark.parametrize("xt,gt", [(BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
+def test_long_rows(bl, M, K, xt, gt):
+    """The gradient in two readings: accesses of every size, fewer rows than a CTA has warps and more."""
+    x, w, b, dy = _inputs(M, K, xt, gt, M + K)
+    y, mean, rstd = _forward(bl, x, w, b, gt)
+    _check_forward(y, mean, rstd, x, w, b, gt, f"{M}x{K}")
+    _check_backward(bl.layer_norm_backward(x.cuda(), w.cuda(), mean, rstd, dy.cuda()), x, w, dy, f"{M}x{K}")
