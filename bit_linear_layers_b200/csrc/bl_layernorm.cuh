@@ -37,7 +37,7 @@ constexpr int kNormGradMaxK = 8192;     // ... (gradient)
 // turn.
 // Bound by memory from 512 columns on (65536 x 256 fp32: 20.6 us, 16384 x 1024:
 // 19.3 us, the copy rate), below that and for bf16 rows by the latency of the
-// two sums with 16 warps per SM (4096 x 4096 bf16: 14.7 us, 4.6 TB/s). One row
+// two sums with 16 warps per SM (4096 x 4096 bf16: 15.1 us, 4.5 TB/s). One row
 // of 4096 takes 2.3 us.
 template <typename TX, int E, int CPT, int W>
 struct NormCfg {
