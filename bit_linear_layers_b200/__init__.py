@@ -497,7 +497,8 @@ def grad_clip(tensors, max_norm: float, *, out=None, stats=None, ws=None):
     (norm + 1e-6)), norm the 2-norm over all of them: in place, or into the
     tensors of `out` (one for each; None: not written). Returns (norm, coef)
     as fp32 device scalars (the two elements of `stats`); nothing waits for
-    the GPU. A NaN among the gradients makes everything NaN."""
+    the GPU. A NaN among the gradients makes everything NaN, an infinity makes
+    coef 0; with max_norm=inf coef is 1 unless the norm is NaN."""
     return _native.grad_clip(list(tensors), None if out is None else list(out), False, max_norm, stats, ws)
 
 

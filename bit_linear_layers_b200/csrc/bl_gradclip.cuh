@@ -1,6 +1,7 @@
 // The 2-norm over many gradient tensors, and the gradients scaled down to a
 // largest norm:
 //   n = sqrt(sum g^2 over all tensors), c = min(1, max_norm / (n + 1e-6)), out = c g
+// (c = 1 where max_norm is infinite and n no NaN).
 //
 // Squares of fp32 and bf16 values span twice the type's exponents, so an fp32
 // sum overflows from |g| = 1.8e19 on and loses what is below 1e-19. The values
@@ -243,7 +244,8 @@ __global__ void __launch_bounds__(kGcThreads)
   for (int i = threadIdx.x; i < num_sums; i += kGcThreads) s += sums[i];
   const double norm = sqrt(gc_block_sum(s, sh));
   double c = static_cast<double>(max_norm) / (norm + 1e-6);
-  c = c > 1.0 ? 1.0 : c;  // NaN stays NaN
+  // 1 also where both are infinite: no norm is above an infinite bound. A NaN norm stays NaN
+  if (!(c <= 1.0) && !isnan(norm)) c = 1.0;
   const float coef = static_cast<float>(c);
   if (stats && blockIdx.x == 0 && threadIdx.x == 0) {
     stats[0] = static_cast<float>(norm);

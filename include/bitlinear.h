@@ -397,8 +397,9 @@ int bl_embedding_backward(const void* ids, int id_type, const void* dy, int dy_t
  * infinity above the largest float) and coef. Sums of squares are fp64, so
  * the norm holds at any scale of g. A gradient that holds a NaN makes norm,
  * coef and every out NaN; one that holds an infinity makes coef 0. Nothing
- * is written in place where coef is 1. max_norm >= 0 (infinity: the norm
- * alone). ws: bl_workspace_bytes(BL_OP_GRAD_CLIP, num_tensors, 0, 0) bytes,
+ * is written in place where coef is 1. max_norm >= 0; an infinite max_norm
+ * gives the norm alone: coef is 1 (NaN if the norm is), infinities among the
+ * gradients included. ws: bl_workspace_bytes(BL_OP_GRAD_CLIP, num_tensors, 0, 0) bytes,
  * 16-byte aligned, not shared with a call still running.
  */
 typedef struct bl_grad_tensor {
