@@ -23,7 +23,7 @@
 
 namespace bl {
 
-// an id in [0, V) as a row index, or -1 (recorded) where it is outside
+// an id in [0, V) as a row index, or -1 where it is outside
 template <typename TI>
 __device__ __forceinline__ int64_t embed_row(const TI* ids, int64_t t, int64_t V) {
   const int64_t id = static_cast<int64_t>(ids[t]);
@@ -145,10 +145,12 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t smem_addr, uint32_t 
   return v;
 }
 
+__device__ __forceinline__ uint32_t embed_key_of(int64_t id, uint32_t V, int64_t padding_id) {
+  return id >= 0 && id < V && id != padding_id ? static_cast<uint32_t>(id) : V;
+}
 template <typename TI>
 __device__ __forceinline__ uint32_t embed_key(const TI* ids, uint32_t i, uint32_t V, int64_t padding_id) {
-  const int64_t id = static_cast<int64_t>(ids[i]);
-  return id >= 0 && id < V && id != padding_id ? static_cast<uint32_t>(id) : V;
+  return embed_key_of(static_cast<int64_t>(ids[i]), V, padding_id);
 }
 
 template <typename TI>
@@ -324,7 +326,9 @@ __global__ void __launch_bounds__(kErThreads)
 
 // Zeros in the rows of the table that no token names: CTA z of nz takes a
 // contiguous range of rows, whose bits it sets from the whole list of tokens. It
-// uses nothing of the sort and does not wait for it. 253 MB of zeros take about
+// uses nothing of the ordering, and runs ahead of its caller's wait for it: it
+// reads the ids (from L2, where the kernels ahead have left them) and writes rows
+// of the table, neither of which the ordering writes. 253 MB of zeros take about
 // 44 us (5.8 TB/s).
 constexpr int kEgThreads = 256;
 constexpr int kEgWarps = kEgThreads / 32;
@@ -343,7 +347,7 @@ __device__ __forceinline__ void embed_zero(uint32_t* bits, const void* __restric
     auto mark = [&](const auto* id) {
 #pragma unroll 8
       for (uint32_t i = tid; i < T; i += kEgThreads) {
-        const uint32_t k = embed_key(id, i, V, padding_id) - v0;
+        const uint32_t k = embed_key_of(__ldcg(id + i), V, padding_id) - v0;
         if (k < rows) atomicOr(&bits[k >> 5], 1u << (k & 31));
       }
     };
@@ -425,8 +429,16 @@ struct EgRow<uint16_t, 8> {
   }
 };
 
-// The first `zero_ctas` CTAs write zeros. Launched with programmatic
-// serialisation: the zeros are written while the list is sorted.
+// The first `zero_ctas` CTAs write zeros, while the list is ordered. What allows
+// that: this grid is scheduled once every CTA of the kernel ahead has let it be,
+// which each does after its own wait (grid_begin), so whatever was enqueued
+// before the two is complete by then, its results are in L2, and nothing reads
+// the table's old rows any more; the kernel ahead writes only the workspace. The
+// CTAs that use its list wait for it first, the others before they end: the grid
+// is complete only after the one ahead, for the kernels that wait for this one
+// (the next may be scheduled at once, and does).
+// (With every zero behind a wait, half of them written by CTAs of the ordering's own
+// grid: 2048 tokens x 2048 columns 49 -> 55 us, 16384 x 2048 65 -> 78 us.)
 template <typename TG, typename TT, int E, int CH, bool ACC>
 __global__ void __launch_bounds__(kEgThreads, 3)
     embed_grad_kernel(const void* __restrict__ ids, bool ids64, int64_t padding_id, uint32_t zero_ctas,
@@ -436,8 +448,11 @@ __global__ void __launch_bounds__(kEgThreads, 3)
   grid_dependents_launch();
   if constexpr (!ACC) {
     __shared__ uint32_t bits[kEzRows / 32];
-    if (blockIdx.x < zero_ctas)
-      return embed_zero<TT, E == 8 ? 8 : 1>(bits, ids, ids64, T, V, padding_id, dtable, D, blockIdx.x, zero_ctas);
+    if (blockIdx.x < zero_ctas) {
+      embed_zero<TT, E == 8 ? 8 : 1>(bits, ids, ids64, T, V, padding_id, dtable, D, blockIdx.x, zero_ctas);
+      grid_dependency_wait();
+      return;
+    }
   }
   constexpr int NC = kEgCols / (32 * E);  // accesses per lane
   constexpr uint32_t BATCH = E == 8 && sizeof(TG) == 2 ? 8 : 4;  // rows in flight
