@@ -5,7 +5,8 @@ and for the short full-precision operators the native ``_native.so``. Each
 function marshals torch tensors into device pointers and the current
 CUDA stream and calls the entry point of the same name; every step of the
 computation runs in the library's CUDA kernels. There is no CPU fallback:
-if the library is missing, importing the binding raises.
+if the library is missing, importing the binding raises; where the native one
+is missing or does not load, the first call that needs it does.
 
     bin_pack(W, mode)                      -> packed, alpha[, beta]
     bin_linear_w1a16(x, packed, alpha)     -> y (bf16)
@@ -27,6 +28,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -145,17 +147,24 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+_native = None
+_native_lock = threading.Lock()
+
+
 def _load_native():
-    """The native binding of the full-precision operators (csrc/bl_binding.cpp)."""
-    if not os.path.exists(NATIVE_PATH):
-        raise ImportError(f"{NATIVE_PATH} is missing: build it with `python bit_linear_layers_b200/build.py`")
-    spec = importlib.util.spec_from_file_location("bit_linear_layers_b200._native", NATIVE_PATH)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    return mod
-
-
-_native = _load_native()
+    """The native binding of the full-precision operators (csrc/bl_binding.cpp), loaded by the first call of one of
+    them: it is built against one version of torch, which the other entry points do not depend on."""
+    global _native
+    with _native_lock:
+        if _native is None:
+            if not os.path.exists(NATIVE_PATH):
+                raise ImportError(f"{NATIVE_PATH} is missing: build it with `python bit_linear_layers_b200/build.py`")
+            spec = importlib.util.spec_from_file_location("bit_linear_layers_b200._native", NATIVE_PATH)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.set_error(BitLinearError)
+            _native = mod
+    return _native
 
 
 def status_string(status: int) -> str:
@@ -453,7 +462,6 @@ def bin_xnor_gemm(a: torch.Tensor, b: torch.Tensor, K: int, *, out=None):
 
 # ---- full-precision operators of a training step
 # The checks of arguments, the allocations and the calls are in csrc/bl_binding.cpp.
-_native.set_error(BitLinearError)
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
@@ -464,7 +472,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     `out`, which may be x. With stats=True returns (y, mean, rstd), the fp32
     [M] statistics that layer_norm_backward takes; mean and rstd, where
     given, receive them."""
-    return _native.layer_norm(x, weight, bias, eps, out, out_dtype, stats, mean, rstd)
+    return (_native or _load_native()).layer_norm(x, weight, bias, eps, out, out_dtype, stats, mean, rstd)
 
 
 def layer_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor, rstd: torch.Tensor,
@@ -473,14 +481,14 @@ def layer_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, mean: torc
     """Gradients of layer_norm: returns (dx [M, K] of x's type or None,
     dweight [K] fp32 or None, dbias [K] fp32 or None). mean and rstd are the
     statistics the forward pass returned."""
-    return _native.layer_norm_backward(x, weight, mean, rstd, dy, want_dx, want_dw, dx, dweight, dbias, ws)
+    return (_native or _load_native()).layer_norm_backward(x, weight, mean, rstd, dy, want_dx, want_dw, dx, dweight, dbias, ws)
 
 
 def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, out=None, out_dtype=None):
     """y = scale * table[ids]: ids int32 or int64 of any shape, table [V, D]
     bf16 or fp32; y [*ids.shape, D] of out_dtype (default: the table's). Ids
     outside [0, V) give rows of zeros and are recorded in device_error()."""
-    return _native.embedding(ids, table, scale, out, out_dtype)
+    return (_native or _load_native()).embedding(ids, table, scale, out, out_dtype)
 
 
 def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, V: int, *, scale: float = 1.0,
@@ -489,7 +497,7 @@ def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, V: int, *, scale: fl
     out_dtype (default: fp32), row v = scale * the sum of dy over the tokens
     that equal v, zeros elsewhere. With accumulate=True the sums are added to
     `out`. Tokens equal to padding_id give nothing."""
-    return _native.embedding_backward(ids, dy, V, scale, padding_id, out, out_dtype, accumulate, ws)
+    return (_native or _load_native()).embedding_backward(ids, dy, V, scale, padding_id, out, out_dtype, accumulate, ws)
 
 
 def grad_clip(tensors, max_norm: float, *, out=None, stats=None, ws=None):
@@ -499,12 +507,12 @@ def grad_clip(tensors, max_norm: float, *, out=None, stats=None, ws=None):
     as fp32 device scalars (the two elements of `stats`); nothing waits for
     the GPU. A NaN among the gradients makes everything NaN, an infinity makes
     coef 0; with max_norm=inf coef is 1 unless the norm is NaN."""
-    return _native.grad_clip(list(tensors), None if out is None else list(out), False, max_norm, stats, ws)
+    return (_native or _load_native()).grad_clip(list(tensors), None if out is None else list(out), False, max_norm, stats, ws)
 
 
 def grad_norm(tensors, *, stats=None, ws=None):
     """The 2-norm over all elements of the tensors, as an fp32 device scalar."""
-    return _native.grad_clip(list(tensors), None, True, float("inf"), stats, ws)[0]
+    return (_native or _load_native()).grad_clip(list(tensors), None, True, float("inf"), stats, ws)[0]
 
 
 def device_error(clear: bool = True, device=None) -> tuple[int, int]:
