@@ -55,11 +55,14 @@ int type_code(const Tensor& t, const char* name, const at::Device& dev) {
 
 int id_code(const Tensor& t, const at::Device& dev) {
   on_device(t, "ids", dev);
-  if (!t.is_contiguous()) refuse("ids must be contiguous");
   if (t.scalar_type() == at::kInt) return BL_IDS_I32;
   if (t.scalar_type() == at::kLong) return BL_IDS_I64;
   refuse("ids must be int32 or int64, got ", t.scalar_type());
 }
+
+// ids in the order of their shape: as they are where they lie so, else a copy (a few bytes for each row of D
+// columns that is looked up or added); made under the device's guard, on the current stream
+Tensor dense_ids(const Tensor& t) { return t.is_contiguous() ? t : t.contiguous(); }
 
 // row pitch of an [M, K] tensor whose rows are dense
 int64_t row_pitch(const Tensor& t, int64_t M, int64_t K, const char* name) {
@@ -166,7 +169,8 @@ Tensor embedding(const Tensor& ids, const Tensor& table, double scale, OptTensor
   const int yt = type_code(*out, "out", dev);
   if (out->sizes() != at::IntArrayRef(shape) || !out->is_contiguous())
     refuse("out must be a contiguous tensor of shape ", at::IntArrayRef(shape));
-  check("bl_embedding", bl_embedding(ids.const_data_ptr(), it, table.const_data_ptr(), tt, out->data_ptr(), yt,
+  const Tensor id = dense_ids(ids);
+  check("bl_embedding", bl_embedding(id.const_data_ptr(), it, table.const_data_ptr(), tt, out->data_ptr(), yt,
                                      ids.numel(), V, D, static_cast<float>(scale), stream_of(dev)));
   return *out;
 }
@@ -191,8 +195,9 @@ Tensor embedding_backward(const Tensor& ids, const Tensor& dy, int64_t V, double
   if (out->dim() != 2 || out->size(0) != V || out->size(1) != D || !out->is_contiguous())
     refuse("out must be a contiguous tensor of shape [", V, ", ", D, "]");
   const Tensor w = workspace(BL_OP_EMBEDDING_BACKWARD, T, V, D, dev, ws);
+  const Tensor id = dense_ids(ids);
   check("bl_embedding_backward",
-        bl_embedding_backward(ids.const_data_ptr(), it, dy.const_data_ptr(), gt, out->data_ptr(), tt, T, V, D,
+        bl_embedding_backward(id.const_data_ptr(), it, dy.const_data_ptr(), gt, out->data_ptr(), tt, T, V, D,
                               static_cast<float>(scale), padding_id.value_or(-1), accumulate ? BL_EMBED_ACCUMULATE : 0u,
                               w.data_ptr(), static_cast<size_t>(w.numel()), stream_of(dev)));
   return *out;
@@ -217,7 +222,8 @@ py::tuple grad_clip(const py::list& tensors, const std::optional<py::list>& outs
   for (size_t i = 0; i < n; ++i) {
     const Tensor& t = tensor_at(tensors, i, "tensors");
     const int code = type_code(t, "tensors", dev);
-    if (!t.is_contiguous()) refuse("tensors must be contiguous");
+    // the elements' order does not matter, only that they fill one run of memory
+    if (t.layout() != at::kStrided || !t.is_non_overlapping_and_dense()) refuse("tensors must be dense");
     bl_grad_tensor& r = rows[i];
     r.numel = t.numel();
     r.type = code;
@@ -229,8 +235,8 @@ py::tuple grad_clip(const py::list& tensors, const std::optional<py::list>& outs
     } else if (PyList_GET_ITEM(outs->ptr(), static_cast<Py_ssize_t>(i)) != Py_None) {
       const Tensor& o = tensor_at(*outs, i, "outputs");
       if (!o.is_cuda() || o.device() != dev || o.scalar_type() != t.scalar_type() || o.numel() != r.numel ||
-          !o.is_contiguous())
-        refuse("an output must be a contiguous tensor of its gradient's type, size and device");
+          !((t.is_contiguous() && o.is_contiguous()) || (o.sizes() == t.sizes() && o.strides() == t.strides())))
+        refuse("an output must be a dense tensor of its gradient's type, size, layout and device");
       r.out = o.data_ptr();
     }
   }
