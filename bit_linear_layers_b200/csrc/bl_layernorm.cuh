@@ -27,20 +27,23 @@ constexpr int kNormGradMaxK = 8192;     // ... (gradient)
 
 // Rows staged on chip. A group of W warps takes a row: the row is copied into
 // shared memory S - 1 rows ahead of its use, CPT columns per thread in units of
-// E, unpacked once where a thread has no more than 32 columns, and passed over
-// three times in registers. A few warps per row leave little beside the
-// arithmetic itself: with eight, the sums' shuffles and barriers took more
-// instructions than the row. The weight and the bias stay in registers up to 16
+// E, unpacked once, and passed over three times in registers (2048 x 11007 bf16:
+// 41 us, 88 us while 32 single columns per thread were indexed at run time and so
+// lay in local memory). A few warps per row leave little beside the arithmetic
+// itself: with eight, the sums' shuffles and barriers took more instructions than
+// the row. The weight and the bias stay in registers up to 16
 // columns per thread, else in shared memory (in planes of four columns, so that
 // a warp's 16-byte reads meet no bank twice); read again for each row they would
 // cost more L2 traffic than the row. The CTAs stay and their groups take rows in
 // turn.
-// Bound by memory from 512 columns on (65536 x 256 fp32: 20.6 us, 16384 x 1024:
-// 19.3 us, the copy rate), below that and for bf16 rows by the latency of the
-// two sums with 16 warps per SM (4096 x 4096 bf16: 15.1 us, 4.5 TB/s). One row
-// of 4096 takes 2.3 us.
+// fp32 rows from 256 columns on are bound by memory (65536 x 256: 20.7 us, 16384 x
+// 1024: 19.5 us, the copy rate); narrower ones and bf16 rows by the latency of the
+// two sums with 16 warps per SM, and bf16 rows of 4096 also by the one row per
+// group that is on its way meanwhile (S = 2: 32 KB per SM; 4096 x 4096 bf16: 15.0
+// us, 4.5 TB/s). One row of 4096 takes 2.7 us in bf16, 2.2 us in fp32.
 template <typename TX, int E, int CPT, int W>
 struct NormCfg {
+  static_assert(CPT <= 32, "a thread's columns stay in registers");
   static constexpr int KP = CPT * W * 32;  // columns a group covers
   static constexpr int SLOT = KP * int(sizeof(TX)) + StagedRow<TX, E>::PAD;
   static constexpr int S = SLOT <= 2080 ? 4 : SLOT <= 4128 ? 3 : 2;
@@ -137,47 +140,41 @@ __global__ void __launch_bounds__((NormCfg<TX, E, CPT, W>::GROUPS * W * 32))
   };
 
   const float inv_k = 1.0f / static_cast<float>(K);
+  constexpr int ALL = NU > 8 ? NU : 8;  // every unit: `held` is in registers only where no index is left
   int slot = 0;
   const TX* xr = x + m * ldx;
   TY* yr = y + m * ldy;
-  constexpr bool HOLD = CPT <= 32;  // few columns: read and unpacked once, held
   for (; m < M; m += step, xr += step * ldx, yr += step * ldy) {
     cp_async_wait<S - 2>();
     group_sync<W>(1 + group);  // the whole row has arrived; the slot of the row before is free
     fetch(slot == 0 ? S - 1 : slot - 1);
     const uint8_t* row = Row::first(ring + slot * C::SLOT, xr);
-    float2 held[HOLD ? NU : 1][PAIRS];
+    float2 held[NU][PAIRS];
     float2 acc = both(0.f);
-#pragma unroll 8
+#pragma unroll ALL
     for (int u = 0; u < NU; ++u) {
       float2 f[PAIRS];
       Row::get_or_zero(row, column(u), T, K, f);
       acc = add2(acc, tree_sum2<PAIRS>(f));
-      if constexpr (HOLD) {
 #pragma unroll
-        for (int j = 0; j < PAIRS; ++j) held[u][j] = f[j];
-      }
+      for (int j = 0; j < PAIRS; ++j) held[u][j] = f[j];
     }
     float s[1] = {acc.x + acc.y};
     group_sums<W>(s, sh[group], warp, 1 + group);
     const float c = s[0] * inv_k;
     float2 a1 = both(0.f), a2[2] = {both(0.f), both(0.f)};
-#pragma unroll 8
+#pragma unroll ALL
     for (int u = 0; u < NU; ++u) {
       float2 f[PAIRS];
-      if constexpr (HOLD) {
 #pragma unroll
-        for (int j = 0; j < PAIRS; ++j) f[j] = held[u][j];
-      } else {
-        Row::get_or_zero(row, column(u), T, K, f);
-      }
+      for (int j = 0; j < PAIRS; ++j) f[j] = held[u][j];
       const int k = column(u);
       // behind the columns 0 - 0
       const float2 cu = make_float2(k < K ? -c : 0.f, (E == 1 ? k + T : k) < K ? -c : 0.f);
 #pragma unroll
       for (int j = 0; j < PAIRS; ++j) {
         f[j] = add2(f[j], cu);
-        if constexpr (HOLD) held[u][j] = f[j];
+        held[u][j] = f[j];
         a2[j & 1] = fma2(f[j], f[j], a2[j & 1]);
       }
       a1 = add2(a1, tree_sum2<PAIRS>(f));
@@ -194,16 +191,12 @@ __global__ void __launch_bounds__((NormCfg<TX, E, CPT, W>::GROUPS * W * 32))
       if (rstd) rstd[m] = r;
     }
     const float2 shift = both(-md * r);
-#pragma unroll 8
+#pragma unroll ALL
     for (int u = 0; u < NU; ++u) {
       const int k = column(u);
       float2 f[PAIRS], wv[PAIRS], bv[PAIRS];
-      if constexpr (HOLD) {
 #pragma unroll
-        for (int j = 0; j < PAIRS; ++j) f[j] = held[u][j];
-      } else {
-        Row::get(row, k, T, f);
-      }
+      for (int j = 0; j < PAIRS; ++j) f[j] = held[u][j];
       if constexpr (C::WB_SMEM) {
         wb_get(wb, k, wv);
         wb_get(wb + C::KP, k, bv);
@@ -216,7 +209,7 @@ __global__ void __launch_bounds__((NormCfg<TX, E, CPT, W>::GROUPS * W * 32))
           wv[j] = make_float2(v0.x, v1.x);
           bv[j] = make_float2(v0.y, v1.y);
         }
-        const float2 z = fma2(HOLD ? f[j] : add2(f[j], both(-c)), both(r), shift);
+        const float2 z = fma2(f[j], both(r), shift);
         f[j] = WB_REGS ? fma2(z, wr[WB_REGS ? u : 0][j], br[WB_REGS ? u : 0][j]) : fma2(z, wv[j], bv[j]);
       }
       if (k < K) put_unit<TY, E>(yr, k, T, K, f);

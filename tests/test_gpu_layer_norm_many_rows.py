@@ -1,4 +1,4 @@
-"""Layer norm and its gradient of narrow rows in such numbers that every slot of a warp's ring of staged rows is
+"""Layer norm and its gradient of rows in such numbers that every slot of a warp's (CTA's) ring of staged rows is
 filled again several times, against the fp64 formulas on the device. The bounds are those of tests/train_ref.py."""
 import pytest
 import torch
@@ -22,12 +22,13 @@ def _inside(got, ref, bound, what):
     assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} outside, first at {bad.nonzero()[0].tolist()}"
 
 
-# 30011 rows: a warp takes seven or more even with eight CTAs of eight warps on each of 148 SMs at 4736 rows a
-# round; the ring has three or four slots. 1030 columns: the tile kernel, whose CTAs come round as often.
-@pytest.mark.parametrize("K", [64, 250, 301, 511, 512, 1030])
+# 60013 rows: a warp takes six or more even with eight CTAs of eight warps on each of 148 SMs, and the ring has three
+# or four slots. 1030 columns: the gradient's tiles, whose CTAs come round as often. From 8192 columns on: one row per
+# CTA at a time, and 32 columns per thread read one by one.
+@pytest.mark.parametrize("K", [64, 250, 301, 511, 512, 1030, 8193, 11008, 16383])
 @pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
 def test_many_rows(bl, K, xt, yt):
-    M = 60013 if K < 1000 else 15013
+    M = 60013 if K < 1000 else 15013 if K < 8000 else 1013
     g = torch.Generator("cuda").manual_seed(K)
 
     def randn(*s):
