@@ -47,6 +47,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -59,6 +60,7 @@ if ROOT not in sys.path:
 
 FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustained": 1400.0}
 CSRC = "bit_linear_layers_b200/csrc/"
+HOST = [CSRC + "bl_common.cuh", CSRC + "bl_host.cuh", CSRC + "bl_api.cu"]  # shared device helpers; launches
 SUSTAINED_AFTER_S = 1.0  # a timed region longer than this runs under the power cap: sustained peak
 
 
@@ -89,10 +91,12 @@ def load_peaks():
 
 
 def src_hash(sources) -> str:
+    """Of the code that a measured kernel is built and launched from; comments and spacing do not count."""
     h = hashlib.sha256()
     for rel in sources:
-        with open(os.path.join(ROOT, rel), "rb") as f:
-            h.update(f.read())
+        with open(os.path.join(ROOT, rel), encoding="utf-8") as f:
+            code = re.sub(r"//[^\n]*|/\*.*?\*/", " ", f.read(), flags=re.S)
+        h.update(" ".join(code.split()).encode())
     return h.hexdigest()[:16]
 
 
@@ -198,7 +202,7 @@ class Decode(Workload):
     metric = "decode GEMV HBM GB/s on packed-weight bytes (W1A16, 1x4096x4096)"
     unit, scale, bound = "GB/s", 1e9, "hbm"
     kernel = "gemv_w1a16_lut_kernel<1> (cluster of 8 x 16 clusters)"
-    sources = [CSRC + "bl_gemv_lut.cuh", CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_gemv_lut.cuh", *HOST]
     traffic_file = "gemv_w1a16_decode_1x4096x4096.traffic.json"
     rotate = 128
 
@@ -283,7 +287,7 @@ class Prefill(Workload):
     metric = "prefill TFLOP/s (W1A16, 7B MLP up + down projections, 2048 tokens)"
     unit, scale, bound = "TFLOP/s", 1e12, "tensor"
     kernel = "gemm_ts_kernel<0,1,256,false> (persistent, 148 CTAs)"
-    sources = [CSRC + "bl_gemm_ts.cuh", CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_gemm_ts.cuh", *HOST]
     traffic_file = "gemm_ts_w1a16_prefill_2048x4096x11008.traffic.json"
     launches_per_step = 2
     rotate = 4
@@ -367,7 +371,7 @@ class Backward(Workload):
     unit, scale, bound = "TFLOP/s", 1e12, "tensor"
     kernel = ("gemm_ts_kernel<0,1,256,false> (dx on transposed signs) + gemm_ss_ste_kernel (dW) + "
               "layout kernels (one call)")
-    sources = [CSRC + "bl_backward.cuh", CSRC + "bl_gemm_ts.cuh", CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_backward.cuh", CSRC + "bl_gemm_ts.cuh", *HOST]
     traffic_file = "ste_backward_2048x4096x11008.traffic.json"  # the dx GEMM launch (largest share of the step)
     launches_per_step = 8  # split, transposed pack, fill, dx GEMM, two transposes, dW GEMM, finalize
     rotate = 2
@@ -461,7 +465,7 @@ class W1A8(Workload):
     unit, scale, bound = "TOP/s", 1e12, "tensor"
     dtype = "s8"
     kernel = "ln_quant_kernel<NV> + gemm_ts_kernel<1,1,256|128,*> (one call; time includes LN + quantisation)"
-    sources = [CSRC + "bl_gemm_ts.cuh", CSRC + "bl_lnquant.cuh", CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_gemm_ts.cuh", CSRC + "bl_lnquant.cuh", *HOST]
     traffic_file = "bitlinear_w1a8_1p3b_512tokens.traffic.json"  # the GEMM launches' DRAM bytes
     launches_per_step = 4
     rotate = 16
@@ -553,7 +557,7 @@ class W1A8Single(Workload):
     unit, scale, bound = "tok/s", 1.0, "hbm"
     dtype = "s8"
     kernel = "bitlinear_small_kernel<4,false> (one fused launch per call)"
-    sources = [CSRC + "bl_gemv.cuh", CSRC + "bl_lnquant.cuh", CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_gemv.cuh", CSRC + "bl_lnquant.cuh", *HOST]
     traffic_file = "bitlinear_small_w1a8_single_4x256x256.traffic.json"
     roof_unit = "GB/s"
     rotate = 18000  # 14 KB per copy: 250 MB, about twice the L2
@@ -743,7 +747,7 @@ class W1A1(Workload):
     unit, scale, bound = "TOP/s", 1e12, "alu"
     dtype = "b1"
     kernel = "xnor_gemm_kernel (64x64 tiles, XOR + POPC on the integer pipes)"
-    sources = [CSRC + "bl_xnor.cuh", CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_xnor.cuh", *HOST]
     traffic_file = "xnor_w1a1_1p3b_512tokens.traffic.json"
     launches_per_step = 2
     rotate = 8
@@ -855,7 +859,7 @@ class DecodeStack(Workload):
     roof_unit = "GB/s"
     kernel = ("gemv_w1a16_stream_kernel (15 clusters of 8 CTAs, persistent; two launches per step: 82 + 46 "
               "levels, at most 144 linears per launch)")
-    sources = [CSRC + "bl_gemv_stream.cuh", CSRC + "bl_gemv_lut.cuh", CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_gemv_stream.cuh", CSRC + "bl_gemv_lut.cuh", *HOST]
     traffic_file = "gemv_w1a16_stream_7b_decode_batch1.traffic.json"
     traffic_per = "step"  # achieved and traffic both cover the step's two launches
     launches_per_step = 2
@@ -946,8 +950,7 @@ class DecodeStack16(DecodeStack):
               "one stacked call per token step)")
     kernel = ("gemv_w1a16_stream_mma_kernel<16> (15 clusters of 8 CTAs, persistent; two launches per step: "
               "82 + 46 levels, at most 144 linears per launch)")
-    sources = [CSRC + "bl_gemv_stream_mma.cuh", CSRC + "bl_gemv_stream.cuh", CSRC + "bl_gemv_mma.cuh",
-               CSRC + "bl_common.cuh", CSRC + "bl_api.cu"]
+    sources = [CSRC + "bl_gemv_stream_mma.cuh", CSRC + "bl_gemv_stream.cuh", CSRC + "bl_gemv_mma.cuh", *HOST]
     traffic_file = "gemv_w1a16_stream_mma_7b_decode_batch16.traffic.json"
 
 
