@@ -486,28 +486,30 @@ def layer_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, mean: torc
 
 def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, out=None, out_dtype=None):
     """y = scale * table[ids]: ids int32 or int64 of any shape and strides (copied
-    first where they are not contiguous), table [V, D] bf16 or fp32, contiguous; y [*ids.shape, D] of out_dtype (default: the table's). Ids
-    outside [0, V) give rows of zeros and are recorded in device_error()."""
+    first where they are not contiguous), table [V, D] bf16 or fp32, contiguous;
+    y [*ids.shape, D] of out_dtype (default: the table's). Ids outside [0, V)
+    give rows of zeros and are recorded in device_error()."""
     return (_native or _load_native()).embedding(ids, table, scale, out, out_dtype)
 
 
 def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, V: int, *, scale: float = 1.0,
                        padding_id: int | None = None, out=None, out_dtype=None, accumulate: bool = False, ws=None):
     """Gradient of embedding with respect to the whole table, from ids as there
-    and dy [*ids.shape, D], contiguous: [V, D] of out_dtype (default: fp32), row v = scale * the sum of dy over the tokens
-    that equal v, zeros elsewhere. With accumulate=True the sums are added to
-    `out`. Tokens equal to padding_id give nothing."""
+    and dy [*ids.shape, D], contiguous: [V, D] of out_dtype (default: fp32), row
+    v = scale * the sum of dy over the tokens that equal v, zeros elsewhere. With
+    accumulate=True the sums are added to `out`. Tokens equal to padding_id give
+    nothing, nor do ids outside [0, V), which are recorded in device_error()."""
     return (_native or _load_native()).embedding_backward(ids, dy, V, scale, padding_id, out, out_dtype, accumulate, ws)
 
 
 def grad_clip(tensors, max_norm: float, *, out=None, stats=None, ws=None):
     """Scale the tensors (bf16 or fp32, one device, each dense: contiguous up to
-    the order of its dimensions) by coef = min(1, max_norm /
-    (norm + 1e-6)), norm the 2-norm over all of them: in place, or into the
-    tensors of `out` (one for each, of its layout; None: not written). Returns (norm, coef)
-    as fp32 device scalars (the two elements of `stats`); nothing waits for
-    the GPU. A NaN among the gradients makes everything NaN, an infinity makes
-    coef 0; with max_norm=inf coef is 1 unless the norm is NaN."""
+    the order of its dimensions) by coef = min(1, max_norm / (norm + 1e-6)), norm
+    the 2-norm over all of them: in place, or into the tensors of `out` (one for
+    each, of its layout; None: not written). Returns (norm, coef) as fp32 device
+    scalars (the two elements of `stats`); nothing waits for the GPU. A NaN among
+    the gradients makes everything NaN, an infinity makes coef 0; with
+    max_norm=inf coef is 1 unless the norm is NaN."""
     return (_native or _load_native()).grad_clip(list(tensors), None if out is None else list(out), False, max_norm, stats, ws)
 
 
